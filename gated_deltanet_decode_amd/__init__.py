@@ -21,6 +21,14 @@ C entry points:
     layer_tail_ba(x, conv_w, conv_state, ba, a_log, dt_bias, state, z, norm_w, y, ...)
                                                  -> gdn_layer_tail_ba
     layer_tail_ba_workspace_bytes(B)             -> gdn_layer_tail_ba_workspace_bytes
+    add_rmsnorm_q8(x, residual, residual_out, norm_w, q, scale) -> gdn_add_rmsnorm_q8
+    quantize_q8(x, q, scale)                     -> gdn_quantize_q8
+    linear_q8(a, a_scale, w, w_scale, outs)      -> gdn_linear_q8
+    verify(target, draft, draft_tokens, u_accept, u_sample, accepted, tokens, ...)
+                                                 -> gdn_verify
+    verify_workspace_bytes(B, V)                 -> gdn_verify_workspace_bytes
+    pair_commit(accepted, state, state_next, conv_state, conv_state_next)
+                                                 -> gdn_pair_commit
     last_error(), version()
 
 If the library has not been built, importing this package raises: there is
@@ -38,7 +46,8 @@ __all__ = ["GdnError", "Dims", "TailParams", "GateInputs", "lib", "step", "bind_
            "layer_tail", "layer_tail_workspace_bytes", "layer_tail_noalloc", "layer_tail_pair",
            "gate_transform",
            "layer_tail_ba",
-           "layer_tail_ba_workspace_bytes", "last_error", "version", "PAGE_DIMS",
+           "layer_tail_ba_workspace_bytes", "add_rmsnorm_q8", "quantize_q8", "linear_q8",
+           "verify", "verify_workspace_bytes", "pair_commit", "last_error", "version", "PAGE_DIMS",
            "PAGE_TAIL", "ERRORS"]
 
 if not os.path.exists(LIBRARY):
@@ -107,6 +116,29 @@ lib.gdn_layer_tail_ba.argtypes = [_DP, _TP, _i32] + [_vp] * 3 + [_GP] + [_vp] * 
     [_vp, ctypes.c_size_t, _vp]
 lib.gdn_layer_tail_ba_workspace_bytes.restype = ctypes.c_size_t
 lib.gdn_layer_tail_ba_workspace_bytes.argtypes = [_DP, _i32]
+
+
+class LinearOut(ctypes.Structure):
+    """gdn_linear_out"""
+    _fields_ = [("out", ctypes.c_void_p), ("n", ctypes.c_int32)]
+
+
+LINEAR_MAX_OUTS = 4
+
+lib.gdn_add_rmsnorm_q8.restype = ctypes.c_int
+lib.gdn_add_rmsnorm_q8.argtypes = [_i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, ctypes.c_float,
+                                   _vp, _vp, _vp]
+lib.gdn_quantize_q8.restype = ctypes.c_int
+lib.gdn_quantize_q8.argtypes = [_i32, _i32, _i32, _vp, _vp, _vp, _vp]
+lib.gdn_linear_q8.restype = ctypes.c_int
+lib.gdn_linear_q8.argtypes = [_i32, _i32] + [_vp] * 5 + [_i32, ctypes.POINTER(LinearOut), _i32,
+                                                         _vp]
+lib.gdn_verify.restype = ctypes.c_int
+lib.gdn_verify.argtypes = [_i32] * 4 + [_vp] * 8 + [_vp, ctypes.c_size_t, _vp]
+lib.gdn_verify_workspace_bytes.restype = ctypes.c_size_t
+lib.gdn_verify_workspace_bytes.argtypes = [_i32, _i32]
+lib.gdn_pair_commit.restype = ctypes.c_int
+lib.gdn_pair_commit.argtypes = [_DP, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp]
 
 
 class GdnError(RuntimeError):
@@ -383,3 +415,194 @@ def layer_tail_ba(x, conv_w, conv_state, ba, a_log, dt_bias, state, z, norm_w, y
         _ptr(dbg_qkv, "dbg_qkv", (B, C), optional=True),
         _ptr(dbg_core, "dbg_core", (B, dims.n_v_heads, dims.d_v), optional=True),
         ws_ptr, ws_bytes, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# The layer around the recurrent branch, in 8 bits, and the verification of a
+# speculative pair.  These take several element types; all tensors of a call
+# must be on one GPU, and the call is made on that GPU's current stream (or
+# the stream given, which must be that GPU's) whichever GPU is current.
+try:
+    _TYPES = {_torch.float32: 0, _torch.bfloat16: 1, _torch.float16: 2}
+    _I8, _I32 = _torch.int8, _torch.int32
+except NameError:
+    _TYPES, _I8, _I32 = {}, None, None
+_NO_TYPE = -1
+
+
+def _addr(t, name, dtype, shape, device):
+    """Device address of a contiguous tensor of the given type and shape on
+    GPU `device`."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == device
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _typed(t, name)
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {str(dtype)[6:]}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on GPU {t.get_device()}, expected GPU {device}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _typed(t, name, types=None):
+    import torch
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if types is not None and t.dtype not in types:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+
+
+def _lead(t, name, ndim, types=None):
+    """The GPU of the tensor that a call's sizes are read from."""
+    if t.__class__ is not _torch.Tensor or not t.is_cuda or (types and t.dtype not in types):
+        _typed(t, name, types)
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions, got shape {tuple(t.shape)}")
+    return t.get_device()
+
+
+def _issue(fn, args, device, stream) -> None:
+    """fn(*args, stream) with GPU `device` current."""
+    if stream is None:
+        raw = _torch._C._cuda_getCurrentRawStream(device)
+    else:
+        on = getattr(stream, "device_index", device)
+        if on != device:
+            raise ValueError(f"stream is on GPU {on}, the tensors are on GPU {device}")
+        raw = _stream(stream)
+    if device == _torch._C._cuda_getDevice():
+        rc = fn(*args, raw)
+    else:
+        with _torch.cuda.device(device):
+            rc = fn(*args, raw)
+    if rc != 0:
+        raise GdnError(rc, last_error())
+
+
+def add_rmsnorm_q8(x, residual, residual_out, norm_w, q, scale, eps=1e-6, stream=None) -> None:
+    """gdn_add_rmsnorm_q8: x [rows][n] and residual (None: no residual) of
+    float32, bfloat16 or float16, residual_out like residual (the same tensor:
+    in place), norm_w [n] float32 -> codes q [rows][n] int8 and scale [rows]
+    float32; q * scale is the normed row times norm_w."""
+    dev = _lead(x, "x", 2, _TYPES)
+    rows, n = shape = x.shape
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out is given without a residual")
+        rtype, rp, ro = _NO_TYPE, None, None
+    else:
+        if getattr(residual, "dtype", None) not in _TYPES:
+            _typed(residual, "residual", _TYPES)
+        rtype = _TYPES[residual.dtype]
+        rp = _addr(residual, "residual", residual.dtype, shape, dev)
+        ro = _addr(residual_out, "residual_out", residual.dtype, shape, dev)
+    _issue(lib.gdn_add_rmsnorm_q8,
+           (rows, n, _TYPES[x.dtype], _addr(x, "x", x.dtype, shape, dev), rtype, rp, ro,
+            _addr(norm_w, "norm_w", _F32, (n,), dev), eps, _addr(q, "q", _I8, shape, dev),
+            _addr(scale, "scale", _F32, (rows,), dev)), dev, stream)
+
+
+def quantize_q8(x, q, scale, stream=None) -> None:
+    """gdn_quantize_q8: x [rows][n] of float32, bfloat16 or float16 -> codes
+    q [rows][n] int8 and scale [rows] float32."""
+    dev = _lead(x, "x", 2, _TYPES)
+    rows, n = shape = x.shape
+    _issue(lib.gdn_quantize_q8,
+           (rows, n, _TYPES[x.dtype], _addr(x, "x", x.dtype, shape, dev),
+            _addr(q, "q", _I8, shape, dev), _addr(scale, "scale", _F32, (rows,), dev)),
+           dev, stream)
+
+
+def linear_q8(a, a_scale, w, w_scale, outs, bias=None, stream=None) -> None:
+    """gdn_linear_q8: a [M][K] int8 with a_scale [M], w [N][K] int8 with w_scale
+    [N] (bias [N] float32 or None) -> outs: a tensor [M][N], or up to four
+    [M][n_i] that take the N channels in order; float32, bfloat16 or float16,
+    all of one type."""
+    dev = _lead(a, "a", 2)
+    M, K = a.shape
+    if not isinstance(outs, (list, tuple)):
+        outs = (outs,)
+    if not 1 <= len(outs) <= LINEAR_MAX_OUTS:
+        raise ValueError(f"outs must be 1 to {LINEAR_MAX_OUTS} tensors, got {len(outs)}")
+    _lead(outs[0], "outs[0]", 2, _TYPES)
+    dtype = outs[0].dtype
+    groups = (LinearOut * len(outs))()
+    N = 0
+    for i, o in enumerate(outs):
+        _lead(o, f"outs[{i}]", 2, _TYPES)
+        n = o.shape[1]
+        groups[i].out = _addr(o, f"outs[{i}]", dtype, (M, n), dev)
+        groups[i].n = n
+        N += n
+    _issue(lib.gdn_linear_q8,
+           (M, K, _addr(a, "a", _I8, (M, K), dev), _addr(a_scale, "a_scale", _F32, (M,), dev),
+            _addr(w, "w", _I8, (N, K), dev), _addr(w_scale, "w_scale", _F32, (N,), dev),
+            None if bias is None else _addr(bias, "bias", _F32, (N,), dev),
+            _TYPES[dtype], groups, len(outs)), dev, stream)
+
+
+def verify_workspace_bytes(B: int, V: int) -> int:
+    return int(lib.gdn_verify_workspace_bytes(B, V))
+
+
+def verify(target, draft, draft_tokens, u_accept, u_sample, accepted, tokens, n_draft=None,
+           workspace=None, stream=None) -> None:
+    """gdn_verify: target [B][K+1][V] and draft [B][K][V] (None: greedy drafts)
+    probabilities of one type (float32, bfloat16 or float16), draft_tokens
+    [B][K] int32, n_draft [B] int32 or None, u_accept [B][K] and u_sample [B]
+    float32 -> accepted [B] and tokens [B][K+1] int32.  workspace: a GPU tensor
+    of at least verify_workspace_bytes(B, V) bytes (any dtype)."""
+    dev = _lead(target, "target", 3, _TYPES)
+    B, K1, V = target.shape
+    K = K1 - 1
+    ws_ptr, ws_bytes = _workspace(workspace)
+    if ws_ptr is not None and workspace.get_device() != dev:
+        raise ValueError(f"workspace is on GPU {workspace.get_device()}, expected GPU {dev}")
+    _issue(lib.gdn_verify,
+           (B, K, V, _TYPES[target.dtype],
+            _addr(target, "target", target.dtype, (B, K1, V), dev),
+            None if draft is None else _addr(draft, "draft", target.dtype, (B, K, V), dev),
+            _addr(draft_tokens, "draft_tokens", _I32, (B, K), dev),
+            None if n_draft is None else _addr(n_draft, "n_draft", _I32, (B,), dev),
+            _addr(u_accept, "u_accept", _F32, (B, K), dev),
+            _addr(u_sample, "u_sample", _F32, (B,), dev),
+            _addr(accepted, "accepted", _I32, (B,), dev),
+            _addr(tokens, "tokens", _I32, (B, K1), dev), ws_ptr, ws_bytes), dev, stream)
+
+
+def pair_commit(accepted, state, state_next, conv_state=None, conv_state_next=None,
+                stream=None) -> None:
+    """gdn_pair_commit: accepted [B] int32; state and state_next [B][Hv][dv][dk]
+    (or [layers][B][Hv][dv][dk]) and, optionally, conv_state and
+    conv_state_next [B][K-1][C] (or [layers][B][K-1][C]): the tentative
+    buffers of the sequences with accepted >= 1 replace the committed ones."""
+    if getattr(state, "ndim", 5) == 4:
+        dev, layers, sh = _lead(state, "state", 4), 1, tuple(state.shape)
+        lead = sh[:1]
+    else:
+        dev = _lead(state, "state", 5)
+        sh = tuple(state.shape)
+        layers, lead = sh[0], sh[:2]
+    B, Hv, dv, dk = sh[-4:]
+    rs, ring = None, 0
+    if conv_state is not None or conv_state_next is not None:
+        _lead(conv_state, "conv_state", len(lead) + 2)
+        rs = lead + tuple(conv_state.shape[len(lead):])
+        ring = rs[-1] * rs[-2]
+    d = Dims(Hv, Hv, dk, dv)           # the copy does not depend on the key heads
+    _issue(lib.gdn_pair_commit,
+           (ctypes.byref(d), layers, B, _addr(accepted, "accepted", _I32, (B,), dev),
+            _addr(state, "state", _F32, sh, dev),
+            _addr(state_next, "state_next", _F32, sh, dev), ring,
+            None if rs is None else _addr(conv_state, "conv_state", _F32, rs, dev),
+            None if rs is None else _addr(conv_state_next, "conv_state_next", _F32, rs, dev)),
+           dev, stream)

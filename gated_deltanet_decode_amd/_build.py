@@ -9,7 +9,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIBRARY = os.path.join(CSRC, "libgdn.so")
 SOURCES = [os.path.join(CSRC, f) for f in
-           ("gdn_api.cpp", "gdn_step.hip", "gdn_seq.hip", "gdn_tail.hip")]
+           ("gdn_api.cpp", "gdn_step.hip", "gdn_seq.hip", "gdn_tail.hip",
+            "gdn_serve_api.cpp", "gdn_quant.hip", "gdn_linear.hip", "gdn_verify.hip")]
 # Measurement aids (a copy of known size and an in-place read-modify-write with
 # the step kernel's access pattern), built as their own library.
 PROBE_LIBRARY = os.path.join(CSRC, "libgdn_probe.so")

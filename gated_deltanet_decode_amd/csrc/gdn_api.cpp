@@ -12,6 +12,7 @@
 #include <cstdint>
 #include <cstdio>
 
+#include "gdn_check.hpp"
 #include "gdn_launch.hpp"
 
 namespace gdn {
@@ -32,11 +33,9 @@ int device_cus() {
     return n;
 }
 
-}  // namespace gdn
-
 namespace {
-
 thread_local char g_error[512];
+}
 
 void clear_error() { g_error[0] = '\0'; }
 
@@ -48,79 +47,25 @@ int fail(int code, const char *fmt, ...) {
     return code;
 }
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// Do [a, a+na) and [b, b+nb) share a byte?
-bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-    if (!a || !b || na == 0 || nb == 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return a0 < b0 + nb && b0 < a0 + na;
-}
-
-struct Buf {
-    const char *name;
-    const void *p;
-    size_t bytes;
-};
-
-// Every output must be disjoint from every other listed buffer.
-int check_alias(const Buf *outs, int n_out, const Buf *all, int n_all) {
-    for (int i = 0; i < n_out; ++i)
-        for (int j = 0; j < n_all; ++j) {
-            if (outs[i].p == all[j].p && outs[i].name == all[j].name) continue;  // itself
-            if (overlap(outs[i].p, outs[i].bytes, all[j].p, all[j].bytes))
-                return fail(GDN_ERR_ALIAS, "%s overlaps %s", outs[i].name, all[j].name);
-        }
-    return GDN_OK;
-}
-
-int check_dims(const gdn_dims *d) {
-    if (!d) return fail(GDN_ERR_NULL, "dims is NULL");
-    if (d->n_v_heads < 1 || d->n_k_heads < 1)
-        return fail(GDN_ERR_SHAPE, "head counts must be >= 1 (n_v_heads=%d, n_k_heads=%d)",
-                    d->n_v_heads, d->n_k_heads);
-    if (d->n_v_heads % d->n_k_heads != 0)
-        return fail(GDN_ERR_SHAPE, "n_v_heads=%d is not a multiple of n_k_heads=%d",
-                    d->n_v_heads, d->n_k_heads);
-    if (d->d_k != gdn::kHeadDim || d->d_v != gdn::kHeadDim)
-        return fail(GDN_ERR_SHAPE, "only d_k = d_v = %d is supported (got d_k=%d, d_v=%d)",
-                    gdn::kHeadDim, d->d_k, d->d_v);
-    return GDN_OK;
-}
-
-// Heads of one call map to workgroups along grid x, and the persistent
-// kernels count 16 row tiles per head in a 32-bit index that may run up to
-// one grid stride (at most 65536 tiles) past the last tile.
-int check_batch(const gdn_dims *d, int64_t B, const char *what) {
-    if (B < 1) return fail(GDN_ERR_SHAPE, "%s must be >= 1 (got %lld)", what, (long long)B);
-    const int64_t limit = (static_cast<int64_t>(INT32_MAX) - 65536) / 16;   // 134213631
-    if (B * d->n_v_heads > limit)
-        return fail(GDN_ERR_SHAPE, "B * n_v_heads = %lld exceeds %lld",
-                    (long long)(B * d->n_v_heads), (long long)limit);
-    return GDN_OK;
-}
-
-#define GDN_TRY(expr)               \
-    do {                            \
-        const int rc__ = (expr);    \
-        if (rc__ != GDN_OK) return rc__; \
-    } while (0)
-
-int check_ptrs(const Buf *bufs, int n, uintptr_t align) {
-    for (int i = 0; i < n; ++i) {
-        if (!bufs[i].p) return fail(GDN_ERR_NULL, "%s is NULL", bufs[i].name);
-        if (!aligned(bufs[i].p, align))
-            return fail(GDN_ERR_ALIGN, "%s (%p) is not %u-byte aligned", bufs[i].name, bufs[i].p,
-                        static_cast<unsigned>(align));
-    }
-    return GDN_OK;
-}
-
 int hip_status(hipError_t e, const char *what) {
     if (e != hipSuccess)
         return fail(GDN_ERR_HIP, "%s: %s (%d)", what, hipGetErrorString(e), static_cast<int>(e));
     return GDN_OK;
 }
+
+}  // namespace gdn
+
+namespace {
+
+using gdn::Buf;
+using gdn::aligned;
+using gdn::check_alias;
+using gdn::check_batch;
+using gdn::check_dims;
+using gdn::check_ptrs;
+using gdn::clear_error;
+using gdn::fail;
+using gdn::hip_status;
 
 // gdn_seq and gdn_seq_exact: checks, then the launch (exact: no scaled groups).
 int seq_call(const char *name, bool exact, const gdn_dims *dims, int32_t B, int32_t T,
@@ -194,7 +139,7 @@ extern "C" {
 
 int gdn_version(void) { return GDN_VERSION; }
 
-const char *gdn_last_error(void) { return g_error; }
+const char *gdn_last_error(void) { return gdn::g_error; }
 
 int gdn_step(const gdn_dims *dims, int32_t B, const float *q, const float *k, const float *v,
              const float *beta, const float *gate, float *state, float *out, void *stream) {

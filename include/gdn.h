@@ -13,7 +13,8 @@
  * sequence and layer.
  *
  * Conventions shared by every call
- *   - All tensors are float32 (IEEE binary32), row-major and contiguous.
+ *   - All tensors are float32 (IEEE binary32), row-major and contiguous,
+ *     unless a call names another element type.
  *   - Every pointer is a device pointer (hipMalloc'd or torch CUDA memory)
  *     that the caller owns; the library keeps no reference after the call.
  *   - Tensor pointers must be 16-byte aligned; per-head vectors (beta, gate,
@@ -57,7 +58,7 @@
 extern "C" {
 #endif
 
-#define GDN_VERSION 10300 /* 1.3.0 */
+#define GDN_VERSION 10400 /* 1.4.0 */
 
 #define GDN_OK 0
 #define GDN_ERR_NULL (-1)      /* a required pointer is NULL                  */
@@ -340,6 +341,144 @@ int gdn_layer_tail_noalloc(const gdn_dims *dims, const gdn_tail_params *params, 
                            const float *beta, const float *gate, float *state,
                            const float *z, const float *norm_w, float *y,
                            float *dbg_qkv, float *dbg_core, void *stream);
+
+/*
+ * The layer around the recurrent branch, in 8 bits: the normed and quantised
+ * input, the projections, and what follows a speculative pair (which draft is
+ * accepted, and the states that move with it).  One decoded layer is
+ *   gdn_add_rmsnorm_q8 -> gdn_linear_q8 (x | z | ba) -> gdn_gate_transform,
+ *   gdn_layer_tail or gdn_layer_tail_pair -> gdn_quantize_q8 -> gdn_linear_q8.
+ * None of these calls needs the head geometry.  They follow the conventions
+ * above; element types are named by the codes below (any other code:
+ * GDN_ERR_SHAPE).
+ */
+#define GDN_F32 0  /* IEEE binary32 */
+#define GDN_BF16 1 /* bfloat16      */
+#define GDN_F16 2  /* IEEE binary16 */
+#define GDN_NONE (-1)
+
+/*
+ * gdn_add_rmsnorm_q8 - residual addition, RMS norm and 8-bit codes of `rows`
+ * rows of n elements:
+ *   h = x + residual rounded to the residual's type (h = x without one),
+ *   g_i = h_i * norm_w[i],  G = max_i |g_i|,
+ *   q_i = rint(127 * g_i / G) (ties to even),
+ *   scale = G / 127 / sqrt(mean(h^2) + eps),
+ * so q_i * scale is the normed row times the weight to half a step.  The
+ * root mean square divides out of the codes: they depend on the products g_i
+ * alone, which are formed and compared in binary64, so the codes are the
+ * formula's exactly and do not depend on how the row is summed.  A row whose
+ * products are all zero gets q = 0 and scale = 0; a row with a NaN or an
+ * infinity gets q = 0 and scale = NaN.
+ *   x             [rows][n]  of x_type
+ *   residual      [rows][n]  of residual_type; NULL with residual_type
+ *                            GDN_NONE: no residual
+ *   residual_out  [rows][n]  of residual_type, receives h: may be `residual`
+ *                            itself (in place); NULL exactly when residual is
+ *   norm_w        [n]        float32
+ *   q             [rows][n]  int8, output
+ *   scale         [rows]     float32, output
+ * Pointer alignment: 16 bytes, norm_w and scale 4.  Limits (GDN_ERR_SHAPE
+ * beyond): 1 <= rows <= 4194303, n >= 1, eps finite and >= 0.
+ */
+int gdn_add_rmsnorm_q8(int32_t rows, int32_t n, int32_t x_type, const void *x,
+                       int32_t residual_type, const void *residual, void *residual_out,
+                       const float *norm_w, float eps, int8_t *q, float *scale, void *stream);
+
+/*
+ * gdn_quantize_q8 - the 8-bit codes alone: gdn_add_rmsnorm_q8 with g = x and
+ * scale = G / 127 (the layer tail's y before the output projection).
+ */
+int gdn_quantize_q8(int32_t rows, int32_t n, int32_t x_type, const void *x, int8_t *q,
+                    float *scale, void *stream);
+
+/* One group of output channels of gdn_linear_q8. */
+typedef struct {
+    void *out; /* [M][n] */
+    int32_t n; /* output channels of this group, >= 1 */
+} gdn_linear_out;
+
+#define GDN_LINEAR_MAX_OUTS 4
+
+/*
+ * gdn_linear_q8 - product of 8-bit rows with 8-bit weights:
+ *   y[m][c] = (sum_k a[m][k] * w[c][k]) * a_scale[m] * w_scale[c] + bias[c].
+ * The integer sum is exact (32 bits hold it up to the K limit); the scaling is
+ * binary32, in the order written, rounded once to out_type.
+ *   a        [M][K]  int8       a_scale  [M]  float32
+ *   w        [N][K]  int8       w_scale  [N]  float32
+ *   bias     [N]     float32, optional (NULL = none)
+ *   outs     n_outs groups (1..GDN_LINEAR_MAX_OUTS) that take the N channels
+ *            in order, each a contiguous [M][n] tensor of out_type: the
+ *            layer's x, z and ba come out of one product as gdn_layer_tail_ba
+ *            takes them.  N is the sum of the groups' n.
+ * Pointer alignment: a, w and the outputs 16 bytes, the float32 vectors 4.
+ * Limits (GDN_ERR_SHAPE beyond): M >= 1, 1 <= K <= 131071,
+ * 1 <= N <= 134217727, and ceil(M / 64) * ceil(N / 64) <= 4194303.
+ */
+int gdn_linear_q8(int32_t M, int32_t K, const int8_t *a, const float *a_scale, const int8_t *w,
+                  const float *w_scale, const float *bias, int32_t out_type,
+                  const gdn_linear_out *outs, int32_t n_outs, void *stream);
+
+/*
+ * gdn_verify - speculative verification: which of up to K drafted tokens of
+ * each sequence the target accepts, and the token that follows them, from
+ * given random numbers.  With p_i = target[b][i] and q_i = draft[b][i]:
+ *   drafted token d at position i < n_draft[b] is accepted if all before it
+ *   are and u_accept[b][i] * q_i(d) < p_i(d);
+ *   accepted[b] = a, the number accepted;
+ *   the next token is drawn from w = max(p_a - q_a, 0) if position a refused
+ *   a draft, and from w = p_a if no draft was left; if every w is 0, from p_a:
+ *   the smallest v with w(v) > 0 and w(0) + .. + w(v) > u_sample[b] * sum(w),
+ *   or the largest v with w(v) > 0 if there is none, or -1 if all are 0.
+ * The accepted tokens and the drawn one follow p exactly when the drafts were
+ * drawn from q.  Products, differences and sums are formed in binary64.
+ * Rows need not sum to 1; entries that are negative or not finite count as 0.
+ * A drafted token outside [0, V) is refused.
+ *   target        [B][K+1][V]  of prob_type
+ *   draft         [B][K][V]    of prob_type; NULL: the drafts were not drawn
+ *                              (greedy), q_i is 1 at the drafted token
+ *   draft_tokens  [B][K]       int32
+ *   n_draft       [B]          int32, optional (NULL = K everywhere); values
+ *                              outside [0, K] count as the nearer end
+ *   u_accept      [B][K]       float32 in [0, 1)
+ *   u_sample      [B]          float32 in [0, 1)
+ *   accepted      [B]          int32, output
+ *   tokens        [B][K+1]     int32, output: the accepted drafts, the drawn
+ *                              token, then -1
+ *   workspace     gdn_verify_workspace_bytes(B, V) bytes, 16-byte aligned
+ * Each sequence reads one row of the target and at most one of the draft.
+ * Pointer alignment: target and draft 16 bytes, the others 4.  Limits
+ * (GDN_ERR_SHAPE beyond): 1 <= B <= 65535, 1 <= K <= 1024, V >= 1.  Two calls
+ * that may overlap in time need a workspace each.
+ */
+int gdn_verify(int32_t B, int32_t K, int32_t V, int32_t prob_type, const void *target,
+               const void *draft, const int32_t *draft_tokens, const int32_t *n_draft,
+               const float *u_accept, const float *u_sample, int32_t *accepted, int32_t *tokens,
+               void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace gdn_verify needs (0 on invalid arguments). */
+size_t gdn_verify_workspace_bytes(int32_t B, int32_t V);
+
+/*
+ * gdn_pair_commit - adopts the tentative state of a speculative pair for the
+ * sequences whose draft was accepted: for every b with accepted[b] >= 1 and
+ * every layer, state[b] = state_next[b] and conv_state[b] = conv_state_next[b];
+ * the other sequences' buffers are not written (nor the tentative ones read).
+ *   accepted         [B]  int32 (gdn_verify's)
+ *   state            [layers][B][n_v_heads][d_v][d_k]  in/out
+ *   state_next       the same shape, read
+ *   conv_state       [layers][B][conv_floats]  in/out, optional: NULL together
+ *                    with conv_state_next and conv_floats 0 (gdn_pair has no
+ *                    ring)
+ *   conv_state_next  the same shape, read
+ * conv_floats is (conv_kernel - 1) * C, a multiple of 4.  Limits
+ * (GDN_ERR_SHAPE beyond): layers >= 1, and
+ * layers * B * (2 * n_v_heads + ceil(conv_floats / 8192)) <= 16777215.
+ */
+int gdn_pair_commit(const gdn_dims *dims, int32_t layers, int32_t B, const int32_t *accepted,
+                    float *state, const float *state_next, int32_t conv_floats, float *conv_state,
+                    const float *conv_state_next, void *stream);
 
 /* Message for the last non-zero return on this thread ("" if none). */
 const char *gdn_last_error(void);
