@@ -403,8 +403,10 @@ typedef struct {
 /*
  * gdn_linear_q8 - product of 8-bit rows with 8-bit weights:
  *   y[m][c] = (sum_k a[m][k] * w[c][k]) * a_scale[m] * w_scale[c] + bias[c].
- * The integer sum is exact (32 bits hold it up to the K limit); the scaling is
- * binary32, in the order written, rounded once to out_type.
+ * The integer sum is exact (32 bits hold it up to the K limit).  The scaling is
+ * binary32 in the order written: the sum and its product with a_scale round,
+ * then w_scale and the bias in one fused step; then once to out_type.  The
+ * bits do not depend on M or N.
  *   a        [M][K]  int8       a_scale  [M]  float32
  *   w        [N][K]  int8       w_scale  [N]  float32
  *   bias     [N]     float32, optional (NULL = none)

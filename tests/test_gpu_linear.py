@@ -70,6 +70,30 @@ def test_channel_counts(g, M, N):
     check(g, M, [N], 160, torch.float32, True)
 
 
+# Shapes that reach each kernel and tile on a GPU of 256 compute units, with
+# tokens and channels that end inside a tile and groups that end inside one.
+VARIANTS = [(13, [12289, 31]), (30, [6100, 57, 43]), (30, [12300, 50]), (200, [1999, 51]),
+            (500, [1025, 1025]), (1000, [2050]), (1990, [1000, 40, 1010]), (4100, [2000, 1000, 1999, 1])]
+
+
+@pytest.mark.parametrize("K", [1, 16, 100, 112, 128, 130, 144, 256, 272, 384, 400, 527, 640, 1040])
+@pytest.mark.parametrize("M,splits", VARIANTS)
+def test_every_kernel_over_inner_lengths(g, M, splits, K):
+    check(g, M, splits, K, torch.float32, K % 3 == 0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("K", [527, 1280])
+@pytest.mark.parametrize("M,splits", VARIANTS)
+def test_every_kernel_over_types(g, M, splits, K, dtype):
+    check(g, M, splits, K, dtype, True, full=True)
+
+
+@pytest.mark.parametrize("M,N,K", [(40000, 5, 200), (3, 40000, 33), (9000, 17, 64), (5000, 5000, 48)])
+def test_narrow_and_wide(g, M, N, K):
+    check(g, M, [N], K, torch.float32, False)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("bias", [False, True])
 @pytest.mark.parametrize("M,splits,K", [(1, [8192, 4096, 64], 2048), (5, [33, 1, 7, 100], 100),
