@@ -3,6 +3,8 @@ from __future__ import annotations
 
 import os
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -63,12 +65,22 @@ def build(output: str = LIBRARY, extra=(), verbose: bool = False, sources=None) 
     if sources is None and output == LIBRARY:
         build(PROBE_LIBRARY, extra, verbose, PROBE_SOURCES)
     tmp = output + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, *extra, *(sources or SOURCES), "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"hipcc failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
+
+    # each source on its own, side by side, then one link
+    with tempfile.TemporaryDirectory() as work, ThreadPoolExecutor(os.cpu_count() or 1) as pool:
+        names = list(sources or SOURCES)
+        objects = [os.path.join(work, f"{i}.o") for i in range(len(names))]
+        compile_flags = [f for f in HIPCC_FLAGS if f != "-shared"]
+        list(pool.map(lambda so: run([hipcc(), *compile_flags, *extra, "-c", so[0], "-o", so[1]]),
+                      zip(names, objects)))
+        run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objects, "-o", tmp])
     os.replace(tmp, output)
     return output
 

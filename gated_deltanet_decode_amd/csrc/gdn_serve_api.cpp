@@ -41,7 +41,9 @@ int check_rows(int32_t rows, int32_t n) {
     const int64_t most = UINT32_MAX / gdn::kQuantMaxThreads;   // one workgroup per row
     if (rows < 1 || rows > most)
         return fail(GDN_ERR_SHAPE, "rows must be in [1, %lld] (got %d)", (long long)most, rows);
-    if (n < 1) return fail(GDN_ERR_SHAPE, "n must be >= 1 (got %d)", n);
+    // the kernels' element index stays clear of 2^31
+    if (n < 1 || n > (1 << 30) - 1)
+        return fail(GDN_ERR_SHAPE, "n must be in [1, 1073741823] (got %d)", n);
     return GDN_OK;
 }
 

@@ -379,7 +379,7 @@ int gdn_layer_tail_noalloc(const gdn_dims *dims, const gdn_tail_params *params, 
  *   q             [rows][n]  int8, output
  *   scale         [rows]     float32, output
  * Pointer alignment: 16 bytes, norm_w and scale 4.  Limits (GDN_ERR_SHAPE
- * beyond): 1 <= rows <= 4194303, n >= 1, eps finite and >= 0.
+ * beyond): 1 <= rows <= 4194303, 1 <= n <= 1073741823, eps finite and >= 0.
  */
 int gdn_add_rmsnorm_q8(int32_t rows, int32_t n, int32_t x_type, const void *x,
                        int32_t residual_type, const void *residual, void *residual_out,

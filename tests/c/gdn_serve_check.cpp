@@ -81,10 +81,11 @@ void check_quant() {
                                 reinterpret_cast<float *>(slot(4) + 16), S));
     REFUSED(GDN_ERR_ALIAS, "q", gdn_add_rmsnorm_q8(3, 5, GDN_BF16, slot(0), GDN_F32, slot(1),
             slot(1), F(3), 0.f, C(4), reinterpret_cast<float *>(slot(4) + 12), S));
-    ACCEPTED(gdn_add_rmsnorm_q8(4194303, 2147483647, GDN_F32, slot(0), GDN_NONE, nullptr, nullptr,
+    ACCEPTED(gdn_add_rmsnorm_q8(4194303, 1073741823, GDN_F32, slot(0), GDN_NONE, nullptr, nullptr,
                                 reinterpret_cast<float *>(uintptr_t(1) << 60), 0.f,
                                 reinterpret_cast<int8_t *>(uintptr_t(1) << 61), F(5000), S));
     EXPECT(quant.residual == nullptr && quant.residual_out == nullptr);
+    REFUSED(GDN_ERR_SHAPE, "n must", gdn_quantize_q8(1, 1073741824, GDN_F32, slot(0), C(1), F(2), S));
     REFUSED(GDN_ERR_SHAPE, "rows", gdn_quantize_q8(4194304, 8, GDN_F32, slot(0), C(1), F(2), S));
     ACCEPTED(gdn_quantize_q8(4194303, 8, GDN_F16, slot(0), C(1), F(2), S));
     EXPECT(quant.norm_w == nullptr && quant.x_type == GDN_F16 && quant.residual_type == GDN_NONE);

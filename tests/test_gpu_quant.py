@@ -2,7 +2,9 @@
 The codes have to be the formula's exactly: they are functions of products that
 binary64 holds exactly, and the library divides out every quotient that comes
 near a border.  The scale is one rounding to binary32 of a binary64 value whose
-own error (a sum of n squares) stays below n 2^-53, far under that rounding."""
+own error is that of the sum of squares: at most four roundings of 2^-24 while
+eight squares are added in pairs (squaring, three additions), binary64 above
+that; the square root halves them."""
 import itertools
 
 import numpy as np
@@ -34,13 +36,14 @@ def untouched(whole, fill=77):
     return bool((whole[:GUARD] == fill).all()) and bool((whole[-GUARD:] == fill).all())
 
 
-def check_scale(got, want):
+def check_scale(got, want, norm):
     got = got.cpu().double().numpy()
     nan = np.isnan(want)
     assert np.array_equal(np.isnan(got), nan)
     got, want = got[~nan], want[~nan]
-    # half a binary32 step (2^-150 below the normal range), and the sum's own 2^-53 n
-    lim = np.maximum(want * 2.0 ** -24 * (1 + 1e-4), 2.0 ** -150)
+    # half a binary32 step (2^-150 below the normal range), and half of the sum's
+    # four where there is one
+    lim = np.maximum(want * 2.0 ** -24 * (1 + (2 if norm else 0)) * (1 + 1e-4), 2.0 ** -150)
     assert np.all(np.abs(got - want) <= lim), np.max(np.abs(got - want) / np.maximum(want, 1e-300))
 
 
@@ -77,7 +80,7 @@ def check_norm(g, x, res, w, eps=1e-6, in_place=False):
         assert bool(same.all()), "stored residual"
     wq, ws = sr.rmsnorm_q8(h, w, eps)
     assert np.array_equal(q.cpu().numpy(), wq), "codes"
-    check_scale(s, ws)
+    check_scale(s, ws, True)
 
 
 def check_quant(g, x):
@@ -89,11 +92,11 @@ def check_quant(g, x):
     assert untouched(qw) and untouched(sw)
     wq, ws = sr.quantize_q8(x)
     assert np.array_equal(q.cpu().numpy(), wq), "codes"
-    check_scale(s, ws)
+    check_scale(s, ws, False)
 
 
-WIDTHS = [1, 2, 7, 8, 63, 64, 65, 255, 256, 257, 1000, 2048, 2049, 4096, 4097, 8191, 8192, 16384,
-          20001, 40000]
+WIDTHS = [1, 2, 7, 8, 63, 64, 65, 255, 256, 257, 511, 513, 1000, 1024, 1025, 2048, 2049, 4096, 4097,
+          6001, 6144, 8191, 8192, 8200, 12288, 16384, 16390, 20001, 32768, 32769, 40000]
 
 
 @pytest.mark.parametrize("n", WIDTHS)
@@ -169,9 +172,45 @@ def test_extreme_rows(g, n):
     check_norm(g, x, None, wz)
 
 
+@pytest.mark.parametrize("n", [3, 200, 1024, 2048, 5000, 20000])
+def test_rows_of_every_magnitude(g, n):
+    """Rows scaled by every power of two that binary32 holds, with weights of
+    ordinary size and of 2^40 and 2^-40: products, squares and sums that pass
+    through both ends of the range."""
+    print(f"\n  every magnitude n={n}", flush=True)
+    e = torch.arange(-149, 126, 5 if n < 5000 else 13)
+    x = make(len(e), n, torch.float32, 61).clamp_(-1.9, 1.9) * torch.exp2(e.double()).float()[:, None]
+    w = 1.0 + 0.02 * make(1, n, torch.float32, 62)[0]
+    check_quant(g, x)
+    for s in (1.0, 2.0 ** 40, 2.0 ** -40, 2.0 ** -120):
+        check_norm(g, x, None, w * s)
+        check_norm(g, x, None, w * s, eps=0.0)
+    check_norm(g, x, make(len(e), n, torch.float16, 63) * 1e-3, w)
+
+
+def test_products_that_round_alike(g):
+    """Largest products that differ only beyond binary32: the scale and the codes
+    follow the exact one."""
+    print("\n  products that round alike", flush=True)
+    n = 4096
+    gen = torch.Generator().manual_seed(64)
+    for k in range(6):
+        # h w = (1 + a 2^-12)(1 + b 2^-12) with a + b fixed: equal to 2^-24 or so
+        a = torch.randint(0, 2048, (16, n), generator=gen)
+        h = 1.0 + a.float() * 2.0 ** -12
+        x = h * torch.where(torch.rand(16, n, generator=gen) < 0.5, -1.0, 1.0)
+        w = 1.0 + (2048 - a[0]).float() * 2.0 ** -12
+        x[1:, ::2] *= 0.5
+        x[0] = h[0]
+        check_norm(g, x, None, w)
+        x = torch.full((5, n), 1.0 + k * 2.0 ** -20)        # every element is the largest
+        check_quant(g, x)
+        check_norm(g, x, None, torch.ones(n))
+
+
 def test_rows_do_not_depend_on_the_batch(g):
     print("\n  batch independence", flush=True)
-    for n in (100, 2048, 4096, 9000):
+    for n in (100, 200, 700, 2048, 4096, 5000, 9000, 20000):
         x, w = make(700, n, torch.float32, 41), torch.ones(n)
         r = make(700, n, torch.float32, 42)
         q, s, _ = run_norm(g, x, r, w)
