@@ -51,16 +51,18 @@ struct VerifyArgs {
     const float *u_sample;
     int32_t *accepted;
     int32_t *tokens;
-    double *partial;                 // [B][chunks][2]
+    double *partial;                 // [B][kVerifyUnits] sums, in the workspace
+    int32_t *rows;                   // [B][4] decisions, in the workspace
     int32_t B;
     int32_t K;
     int32_t V;
     int32_t prob_type;
 };
 
-// Entries of a row that one workgroup of the summing kernel takes.
-constexpr int kVerifyChunk = 4096;
-constexpr int64_t verify_chunks(int64_t V) { return (V + kVerifyChunk - 1) / kVerifyChunk; }
+// Units that a row is summed in, at most.
+constexpr int kVerifyUnits = 256;
+// Bytes of workspace a sequence takes: its units' sums and its decision.
+constexpr size_t kVerifyBytes = kVerifyUnits * sizeof(double) + 4 * sizeof(int32_t);
 
 // Copies one sequence's state and ring per accepted sequence and layer.
 struct CommitArgs {

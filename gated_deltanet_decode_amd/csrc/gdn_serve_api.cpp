@@ -195,7 +195,7 @@ int gdn_linear_q8(int32_t M, int32_t K, const int8_t *a, const float *a_scale, c
 
 size_t gdn_verify_workspace_bytes(int32_t B, int32_t V) {
     if (B < 1 || B > 65535 || V < 1) return 0;
-    return static_cast<size_t>(B) * gdn::verify_chunks(V) * 2 * sizeof(double);
+    return static_cast<size_t>(B) * gdn::kVerifyBytes;
 }
 
 int gdn_verify(int32_t B, int32_t K, int32_t V, int32_t prob_type, const void *target,
@@ -246,6 +246,7 @@ int gdn_verify(int32_t B, int32_t K, int32_t V, int32_t prob_type, const void *t
     a.accepted = accepted;
     a.tokens = tokens;
     a.partial = static_cast<double *>(workspace);
+    a.rows = reinterpret_cast<int32_t *>(a.partial + static_cast<size_t>(B) * gdn::kVerifyUnits);
     a.B = B;
     a.K = K;
     a.V = V;

@@ -10,217 +10,349 @@
 //
 // Only one row of the target and at most one of the draft matter to a
 // sequence, once the run of accepted tokens is known, and that takes 2 K
-// single entries.  Two launches: the rows' chunks are summed by a workgroup
-// each, then one workgroup per sequence finds the chunk and the entry in it.
+// single entries.  The row is summed in at most kVerifyUnits units, a wave each;
+// the sums' own cumulative sum names the unit where the goal is passed, and
+// only that unit is read again.  One launch sums the units, a second one picks
+// (a single workgroup a sequence for both was no faster for 32000 entries and
+// twice as slow for 262144; nothing has to be cleared between calls).
 #include "gdn.h"
 #include "gdn_elem.hpp"
+#include "gdn_launch.hpp"
 #include "gdn_serve.hpp"
 
 namespace gdn {
 namespace {
 
-constexpr int kT = 256;
-constexpr int kPer = kVerifyChunk / kT;      // entries of a chunk per thread: 16
+constexpr int kT = 1024;                     // threads of the picking workgroup, K at most
 
 // Negative, infinite and NaN entries count as 0.
 __device__ __forceinline__ double weight(float p) {
-    return p > 0.0f && p <= 3.402823466e38f ? static_cast<double>(p) : 0.0;
+    const float c = fmaxf(p, 0.0f);                       // NaN too
+    return static_cast<double>(c <= 3.402823466e38f ? c : 0.0f);
 }
 
 struct Row {          // what a sequence's next token is drawn from
     int accepted;
-    bool refused;     // position `accepted` refused a draft
+    int refused;      // position `accepted` refused a draft
     int token;        // that draft
 };
 
-// The run of accepted drafts of sequence b.  Called by whole waves; every
-// lane returns the same.
+// The run of accepted drafts of sequence b.  Called by whole waves; every lane
+// returns the same.  Each position's entries are fetched whether or not it has
+// a draft, so that they do not wait for n_draft.
 template <typename PT>
 __device__ __forceinline__ Row decide(const VerifyArgs &a, int64_t b) {
     typedef typename PT::bits bits;
     const int lane = threadIdx.x & 63;
-    int n = a.n_draft ? a.n_draft[b] : a.K;
-    n = max(0, min(n, a.K));
-    Row row{n, false, -1};
-    for (int i0 = 0; i0 < n; i0 += 64) {
+    const int given = a.n_draft ? a.n_draft[b] : a.K;
+    for (int i0 = 0;; i0 += 64) {
         const int i = i0 + lane;
-        bool bad = false;
+        bool good = false;
         int d = -1;
-        if (i < n) {
+        if (i < a.K) {
             d = a.draft_tokens[b * a.K + i];
-            bad = true;
+            const float u = a.u_accept[b * a.K + i];
             if (d >= 0 && d < a.V) {
                 const double p = weight(PT::get(
                     static_cast<const bits *>(a.target)[(b * (a.K + 1) + i) * a.V + d]));
                 const double q = a.draft ? weight(PT::get(
                     static_cast<const bits *>(a.draft)[(b * a.K + i) * a.V + d])) : 1.0;
-                bad = !(static_cast<double>(a.u_accept[b * a.K + i]) * q < p);
+                good = static_cast<double>(u) * q < p;
             }
         }
-        const unsigned long long m = __ballot(bad);
+        const int n = max(0, min(given, a.K));
+        const unsigned long long m = __ballot(i < n && !good);
         if (m) {
             const int first = __ffsll(m) - 1;
-            row.accepted = i0 + first;
-            row.refused = true;
-            row.token = __shfl(d, first, 64);
-            break;
+            return Row{i0 + first, 1, __builtin_amdgcn_readlane(d, first)};
         }
+        if (i0 + 64 >= n) return Row{n, 0, -1};
     }
-    return row;
 }
 
-// The weights at v of the row: `rest` is max(p - q, 0), `all` is p.
+// The weights of the row: max(p - q, 0), or p.
+enum Mode { kPlain, kDraft, kGreedy };    // p; p - q; p less 1 at one entry
 template <typename PT>
 struct Weights {
     typedef typename PT::bits bits;
     const bits *p;
-    const bits *q;     // NULL: no draft row
-    int one;           // the entry where a greedy draft's q is 1, else -1
+    const bits *q;
+    int one;           // the entry where a greedy draft's q is 1
+    int V;
+    Mode mode;
 
     __device__ __forceinline__ Weights(const VerifyArgs &a, int64_t b, const Row &r) {
         p = static_cast<const bits *>(a.target) + (b * (a.K + 1) + r.accepted) * a.V;
-        q = r.refused && a.draft
-                ? static_cast<const bits *>(a.draft) + (b * a.K + r.accepted) * a.V
-                : nullptr;
-        one = r.refused && !a.draft ? r.token : -1;
+        q = static_cast<const bits *>(a.draft) + (b * a.K + r.accepted) * a.V;
+        one = r.token;
+        V = a.V;
+        mode = !r.refused ? kPlain : a.draft ? kDraft : kGreedy;
     }
-    __device__ __forceinline__ void at(int v, double &rest, double &all) const {
-        all = weight(PT::get(p[v]));
-        double d = q ? weight(PT::get(q[v])) : 0.0;
-        if (v == one) d = 1.0;
-        rest = fmax(all - d, 0.0);
+    // N entries from v on as they are stored (kIn: they lie in the row).  A vector
+    // that would pass the row's end is fetched further left, so that no load waits
+    // for a branch; `first` is its first entry.
+    template <int N>
+    struct Raw {
+        typename Pack<bits, N>::vec p, q;
+        int64_t v, first;
+    };
+    template <int N, Mode kMode, bool kIn>
+    __device__ __forceinline__ void fetch(int64_t v, Raw<N> &r) const {
+        r.v = v;
+        r.first = kIn ? v : min(v, static_cast<int64_t>(V) - N);
+        if (kIn || V >= N) {
+            r.p = Pack<bits, N>::load(p + r.first);
+            if constexpr (kMode == kDraft) r.q = Pack<bits, N>::load(q + r.first);
+        } else {                                          // a row shorter than a vector
+            r.p = {};
+            r.q = {};
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (r.first + j >= 0) {
+                    r.p[j] = p[r.first + j];
+                    if constexpr (kMode == kDraft) r.q[j] = q[r.first + j];
+                }
+        }
+    }
+    // The weight of its entry first + j, 0 for those before v.
+    template <int N, Mode kMode, bool kIn>
+    __device__ __forceinline__ double value(const Raw<N> &r, int j) const {
+        double z = weight(PT::get(r.p[j]));
+        if constexpr (kMode == kDraft) z = fmax(z - weight(PT::get(r.q[j])), 0.0);
+        if constexpr (kMode == kGreedy) z = r.first + j == one ? fmax(z - 1.0, 0.0) : z;
+        return kIn || r.first + j >= r.v ? z : 0.0;
+    }
+    template <int N, Mode kMode>
+    __device__ __forceinline__ int64_t at(int64_t v, double (&z)[N]) const {
+        Raw<N> r;
+        fetch<N, kMode, false>(v, r);
+#pragma unroll
+        for (int j = 0; j < N; ++j) z[j] = value<N, kMode, false>(r, j);
+        return r.first;
+    }
+    // N weights from v on, zeros past the row; returns the entry of the first.
+    template <int N>
+    __device__ __forceinline__ int64_t any(int64_t v, double (&z)[N]) const {
+        if (mode == kPlain) return at<N, kPlain>(v, z);
+        if (mode == kDraft) return at<N, kDraft>(v, z);
+        return at<N, kGreedy>(v, z);
     }
 };
 
-// Sums of a chunk's weights: partial[b][chunk] = {sum of rest, sum of all}.
-template <typename PT>
-__global__ __launch_bounds__(kT) void k_verify_sums(VerifyArgs a) {
-    __shared__ double red[2][kT / 64];
-    const int64_t b = blockIdx.y;
-    const Weights<PT> w(a, b, decide<PT>(a, b));
-    const int64_t v0 = static_cast<int64_t>(blockIdx.x) * kVerifyChunk + threadIdx.x * kPer;
-    double rest = 0.0, all = 0.0;
-    for (int j = 0; j < kPer; ++j)
-        if (v0 + j < a.V) {
-            double x, y;
-            w.at(static_cast<int>(v0 + j), x, y);
-            rest += x;
-            all += y;
-        }
-    rest = wave_sum(rest);
-    all = wave_sum(all);
-    if ((threadIdx.x & 63) == 0) {
-        red[0][threadIdx.x >> 6] = rest;
-        red[1][threadIdx.x >> 6] = all;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        double *out = a.partial + (b * gridDim.x + blockIdx.x) * 2;
-        out[0] = ((red[0][0] + red[0][1]) + red[0][2]) + red[0][3];
-        out[1] = ((red[1][0] + red[1][1]) + red[1][2]) + red[1][3];
-    }
+// Within a wave by DPP: moves of a lane's value inside rows of 16 lanes, then
+// the rows' sums by lane reads.
+template <int CTRL>
+__device__ __forceinline__ double dpp(double x) {         // 0 where there is no source lane
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), CTRL, 0xF, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), CTRL, 0xF, 0xF, false);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+__device__ __forceinline__ double lane_of(double x, int l) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b), l);
+    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), l);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+// Inclusive sums over the wave's lanes, and the total.
+__device__ __forceinline__ double scan(double x, double &total) {
+    x += dpp<0x111>(x);                                   // row_shr 1, 2, 4, 8
+    x += dpp<0x112>(x);
+    x += dpp<0x114>(x);
+    x += dpp<0x118>(x);
+    const double r0 = lane_of(x, 15), r1 = lane_of(x, 31), r2 = lane_of(x, 47), r3 = lane_of(x, 63);
+    const int row = (threadIdx.x & 63) >> 4;
+    const double r01 = r0 + r1, r012 = r01 + r2;
+    total = r012 + r3;
+    return (row == 0 ? 0.0 : row == 1 ? r0 : row == 2 ? r01 : r012) + x;
 }
 
-// Inclusive sums over the workgroup's threads, in thread order.
-__device__ __forceinline__ double block_scan(double x, double *red) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+constexpr int kAhead = 4;                    // vectors of a row that a lane fetches at once
+
+template <bool B>
+struct Flag {
+    static constexpr bool value = B;
+};
+
+// The sum of a unit's weights, by one wave; every lane gets the same.
+template <typename PT, Mode kMode>
+__device__ __forceinline__ double unit_sum(const Weights<PT> &w, int64_t v0, int unit) {
+    constexpr int N = 16 / sizeof(typename PT::bits);
+    const int lane = threadIdx.x & 63;
+    double s = 0.0, total;
+    const auto sum = [&](auto in) {
+        constexpr bool kIn = decltype(in)::value;
+        for (int i = 0; i < unit && v0 + i < w.V; i += 64 * N * kAhead) {
+            typename Weights<PT>::template Raw<N> r[kAhead];
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const double y = __shfl_up(x, off, 64);
-        if (lane >= off) x += y;
-    }
-    __syncthreads();                 // red may still be read from a call before
-    if (lane == 63) red[wave] = x;
-    __syncthreads();
-    double base = 0.0;
-    for (int w = 0; w < wave; ++w) base += red[w];
-    return base + x;
+            for (int k = 0; k < kAhead; ++k)
+                w.template fetch<N, kMode, kIn>(v0 + i + (k * 64 + lane) * N, r[k]);
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+                for (int j = 0; j < N; ++j) s += w.template value<N, kMode, kIn>(r[k], j);
+        }
+    };
+    if (v0 + unit <= w.V) sum(Flag<true>{});
+    else sum(Flag<false>{});
+    scan(s, total);
+    return total;
+}
+template <typename PT>
+__device__ __forceinline__ double unit_sum(const Weights<PT> &w, int64_t v0, int unit) {
+    if (w.mode == kPlain) return unit_sum<PT, kPlain>(w, v0, unit);
+    if (w.mode == kDraft) return unit_sum<PT, kDraft>(w, v0, unit);
+    return unit_sum<PT, kGreedy>(w, v0, unit);
 }
 
-// Finds the chunk and the entry where the cumulative sum passes u_sample times
-// the total, and writes the sequence's answer.
+// Finds the unit and the entry where the cumulative sum passes u_sample times the
+// total, and writes the sequence's answer.  sums[0..kVerifyUnits) holds the
+// units' sums, zeros past the last, behind a barrier; the whole workgroup calls.
 template <typename PT>
-__global__ __launch_bounds__(kT) void k_verify_pick(VerifyArgs a, int chunks) {
-    __shared__ double red[kT / 64];
-    __shared__ double total[2], before;
-    __shared__ int chunk, pick, last;
-    const int64_t b = blockIdx.x;
-    const int tid = threadIdx.x;
-    const Row row = decide<PT>(a, b);
-    const double *part = a.partial + b * chunks * 2;
+__device__ __forceinline__ void pick(const VerifyArgs &a, int64_t b, const Row &row, int unit,
+                                     double *sums) {
+    __shared__ double totals[2][kT / 64];
+    __shared__ int at, last;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const float u_sample = a.u_sample[b];
+    const int drafted = tid < a.K ? a.draft_tokens[b * a.K + tid] : -1;   // K <= kT
+    Weights<PT> w(a, b, row);
     if (tid == 0) {
-        chunk = chunks;
-        pick = a.V;
+        at = a.V;
         last = -1;
-        double rest = 0.0, all = 0.0;
-        for (int c = 0; c < chunks; ++c) {
-            rest += part[2 * c];
-            all += part[2 * c + 1];
-        }
-        total[0] = rest;
-        total[1] = all;
     }
-    __syncthreads();
-    const int which = total[0] > 0.0 ? 0 : 1;
-    const double goal = static_cast<double>(a.u_sample[b]) * total[which];
-    if (tid == 0) {
-        double run = 0.0;
-        before = 0.0;
-        for (int c = 0; c < chunks; ++c) {
-            const double x = part[2 * c + which];
-            if (x > 0.0) {
-                chunk = c;            // the last one with a weight, if none passes
-                before = run;
-                if (run + x > goal) break;
-            }
-            run += x;
+    // every wave finds the unit by itself: four sums a lane
+    constexpr int S = kVerifyUnits / 64;
+    double x[S], run, total;
+    for (int turn = 0;; ++turn) {
+        double own = 0.0;
+#pragma unroll
+        for (int j = 0; j < S; ++j) {
+            x[j] = sums[lane * S + j];
+            own += x[j];
         }
+        run = scan(own, total) - own;
+        if (total > 0.0 || w.mode == kPlain) break;
+        // nothing is left of p behind the draft: p itself, seldom
+        w.mode = kPlain;
+        __syncthreads();
+        for (int u = wave; static_cast<int64_t>(u) * unit < w.V; u += kT / 64) {
+            const double s = unit_sum(w, static_cast<int64_t>(u) * unit, unit);
+            if (lane == 0) sums[u] = s;
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    int token = -1;
-    if (chunk < chunks) {
-        const Weights<PT> w(a, b, row);
-        const int64_t v0 = static_cast<int64_t>(chunk) * kVerifyChunk + tid * kPer;
-        double sum = 0.0;
-        for (int j = 0; j < kPer; ++j)
-            if (v0 + j < a.V) {
-                double x, y;
-                w.at(static_cast<int>(v0 + j), x, y);
-                sum += which ? y : x;
+    const double goal = static_cast<double>(u_sample) * total;
+    int hit = -1, end = -1;                               // this lane's first unit past the goal, last live one
+    double hit_base = 0.0, end_base = 0.0;
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+        if (x[j] > 0.0) {
+            end = lane * S + j;
+            end_base = run;
+            if (run + x[j] > goal && hit < 0) {
+                hit = end;
+                hit_base = run;
             }
-        double run = before + (block_scan(sum, red) - sum);
-        int mine = a.V, end = -1;
-        for (int j = 0; j < kPer; ++j)
-            if (v0 + j < a.V) {
-                double x, y;
-                w.at(static_cast<int>(v0 + j), x, y);
-                const double z = which ? y : x;
-                run += z;
-                if (z > 0.0) {
-                    end = static_cast<int>(v0 + j);
-                    if (run > goal && mine == a.V) mine = end;
+        }
+        run += x[j];
+    }
+    int u = -1;                                           // -1: no entry has a weight
+    double base = 0.0;
+    if (const unsigned long long m = __ballot(hit >= 0)) {
+        const int l = __ffsll(m) - 1;
+        u = __builtin_amdgcn_readlane(hit, l);
+        base = lane_of(hit_base, l);
+    } else if (const unsigned long long e = __ballot(end >= 0)) {
+        const int l = 63 - __clzll(e);
+        u = __builtin_amdgcn_readlane(end, l);
+        base = lane_of(end_base, l);
+    }
+    __syncthreads();                                      // at and last are set
+    if (u >= 0) {
+        int found = a.V;
+        end = -1;
+        for (int i = 0, turn = 0; i < unit; i += 4 * kT, turn ^= 1) {
+            const int64_t v = static_cast<int64_t>(u) * unit + i + tid * 4;
+            double z[4], wave_total;
+            const int64_t first = w.any(v, z);
+            const double sum = ((z[0] + z[1]) + z[2]) + z[3];
+            double c = scan(sum, wave_total) - sum;
+            if (lane == 0) totals[turn][wave] = wave_total;
+            __syncthreads();
+            double all = base;
+#pragma unroll
+            for (int k = 0; k < kT / 64; ++k) {
+                if (k == wave) c += all;
+                all += totals[turn][k];
+            }
+            base = all;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                c += z[j];
+                if (z[j] > 0.0) {
+                    end = static_cast<int>(first + j);
+                    if (c > goal) found = min(found, end);
                 }
             }
-        if (mine < a.V) atomicMin(&pick, mine);
+        }
+        if (found < a.V) atomicMin(&at, found);
         if (end >= 0) atomicMax(&last, end);
         __syncthreads();
-        token = pick < a.V ? pick : last;
     }
-    for (int i = tid; i <= a.K; i += kT)
-        a.tokens[b * (a.K + 1) + i] = i < row.accepted    ? a.draft_tokens[b * a.K + i]
-                                      : i == row.accepted ? token
-                                                          : -1;
-    if (tid == 0) a.accepted[b] = row.accepted;
+    const int token = u < 0 ? -1 : at < a.V ? at : last;
+    int32_t *out = a.tokens + b * (a.K + 1);
+    if (tid < a.K) out[tid] = tid < row.accepted ? drafted : tid == row.accepted ? token : -1;
+    if (tid == 0) {
+        out[a.K] = row.accepted == a.K ? token : -1;
+        a.accepted[b] = row.accepted;
+    }
+}
+
+// The units' sums, a wave each, and the decision, for k_verify_pick.
+template <typename PT>
+__global__ __launch_bounds__(256) void k_verify_sums(VerifyArgs a, int unit, int units) {
+    const int64_t b = blockIdx.y;
+    const Row row = decide<PT>(a, b);
+    const Weights<PT> w(a, b, row);
+    for (int u = blockIdx.x * 4 + (threadIdx.x >> 6); u < units; u += gridDim.x * 4) {
+        const double s = unit_sum(w, static_cast<int64_t>(u) * unit, unit);
+        if ((threadIdx.x & 63) == 0) a.partial[b * kVerifyUnits + u] = s;
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        int32_t *r = a.rows + b * 4;
+        r[0] = row.accepted;
+        r[1] = row.refused;
+        r[2] = row.token;
+    }
+}
+template <typename PT>
+__global__ __launch_bounds__(kT) void k_verify_pick(VerifyArgs a, int unit, int units) {
+    __shared__ double sums[kVerifyUnits];
+    const int64_t b = blockIdx.x;
+    const int tid = threadIdx.x;
+    const int32_t *r = a.rows + b * 4;
+    const Row row{r[0], r[1], r[2]};
+    if (tid < kVerifyUnits) sums[tid] = tid < units ? a.partial[b * kVerifyUnits + tid] : 0.0;
+    __syncthreads();
+    pick<PT>(a, b, row, unit, sums);
 }
 
 template <typename PT>
 hipError_t launch(const VerifyArgs &a, hipStream_t s) {
-    const unsigned chunks = static_cast<unsigned>(verify_chunks(a.V));
-    k_verify_sums<PT><<<dim3(chunks, static_cast<unsigned>(a.B)), dim3(kT), 0, s>>>(a);
+    // a unit is what a wave fetches at once, or more where that makes over
+    // kVerifyUnits of them
+    const int64_t step = 64 * kAhead * (16 / sizeof(typename PT::bits));
+    const int64_t turns = (a.V + step * kVerifyUnits - 1) / (step * kVerifyUnits);
+    const int unit = static_cast<int>(step * turns);
+    const int units = static_cast<int>((a.V + static_cast<int64_t>(unit) - 1) / unit);
+    // a wave per unit, or about 2048 workgroups in all (1024 to 8192 within 5 %)
+    const int most = (2048 + a.B - 1) / a.B;
+    const unsigned wide = static_cast<unsigned>(min((units + 3) / 4, most));
+    k_verify_sums<PT><<<dim3(wide, static_cast<unsigned>(a.B)), dim3(256), 0, s>>>(a, unit, units);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    k_verify_pick<PT><<<dim3(static_cast<unsigned>(a.B)), dim3(kT), 0, s>>>(
-        a, static_cast<int>(chunks));
+    k_verify_pick<PT><<<dim3(static_cast<unsigned>(a.B)), dim3(kT), 0, s>>>(a, unit, units);
     return hipGetLastError();
 }
 

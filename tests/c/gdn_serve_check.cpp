@@ -140,7 +140,8 @@ void check_verify() {
     ACCEPTED(gdn_verify(3, 2, 5000, GDN_BF16, slot(0), slot(1), I(2), I(3), F(4), F(5), I(6), I(7),
                         slot(8), need, S));
     EXPECT(verify.B == 3 && verify.K == 2 && verify.V == 5000 && verify.n_draft == I(3) &&
-           verify.partial == reinterpret_cast<double *>(slot(8)) && verify.draft == slot(1));
+           verify.partial == reinterpret_cast<double *>(slot(8)) && verify.draft == slot(1) &&
+           reinterpret_cast<char *>(verify.rows) + 3 * 16 == slot(8) + need);
     ACCEPTED(gdn_verify(3, 2, 5000, GDN_BF16, slot(0), nullptr, I(2), nullptr, F(4), F(5), I(6),
                         I(7), slot(8), need, S));
     EXPECT(verify.draft == nullptr && verify.n_draft == nullptr);

@@ -53,7 +53,9 @@ def check(g, c, n_draft=None):
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("greedy", [False, True])
 @pytest.mark.parametrize("B,K,V", [(1, 1, 1), (3, 2, 5), (64, 1, 100), (40, 3, 4095), (40, 3, 4096),
-                                   (40, 3, 4097), (7, 5, 32000), (5, 1, 131071), (300, 2, 257)])
+                                   (40, 3, 4097), (7, 5, 32000), (5, 1, 131071), (300, 2, 257), (2, 2, 1023),
+                                   (2, 2, 1025), (2, 2, 2047), (2, 2, 2049), (3, 1, 262143), (1, 1, 600001),
+                                   (1, 1, 1100000)])
 def test_against_the_definition(g, dtype, greedy, B, K, V):
     print(f"\n  verify B={B} K={K} V={V} {dtype} greedy={greedy}", flush=True)
     check(g, make(B, K, V, dtype, B + K + V, greedy))
@@ -121,6 +123,26 @@ def test_rows_with_nothing_left(g, V):
     check(g, dict(c, draft=None))
     c["u_accept"][6] = float("nan")
     check(g, c)
+
+
+def test_peaked_rows(g):
+    """Rows where one entry holds nearly everything, at every place of a vector and
+    of a unit, so that the goal falls next to it."""
+    print("\n  verify: peaked rows", flush=True)
+    V = 5000
+    places = list(range(0, 20)) + [63, 64, 255, 256, 1023, 1024, 1025, 2047, 2048, 4095, 4096, 4990, 4999]
+    B = len(places)
+    gen = torch.Generator().manual_seed(5)
+    target = torch.rand(B, 2, V, generator=gen) * 1e-9
+    draft = torch.rand(B, 1, V, generator=gen) * 1e-9
+    for b, v in enumerate(places):
+        target[b, :, v] = 1.0
+    for u in (0.0, 1e-7, 0.5, 0.9999999):
+        c = dict(target=target, draft=draft, draft_tokens=torch.zeros(B, 1).int() + 7,
+                 u_accept=torch.full((B, 1), 0.7), u_sample=torch.full((B,), u))
+        for dt in (torch.float32, torch.bfloat16):
+            check(g, dict(c, target=target.to(dt), draft=draft.to(dt)))
+            check(g, dict(c, target=target.to(dt), draft=None))
 
 
 def test_offsets_past_31_bits(g):

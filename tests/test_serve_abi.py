@@ -136,8 +136,7 @@ def test_verify_validation(g):
     expect(g, f(tok=base["d"] + 8), -4, "draft_tokens")
     expect(g, f(tok=base["acc"] + 4), -4, "accepted")
     expect(g, f(ws=base["target"] + 16), -4, "target")
-    # V past 2^31 / 4096 chunks would still be in range; a workspace that small is not
-    expect(g, f(V=2 ** 31 - 1), -5, "needed")
+    expect(g, f(B=3), -5, "needed")
 
 
 def test_commit_validation(g):
