@@ -12,9 +12,12 @@
 // sequence, once the run of accepted tokens is known, and that takes 2 K
 // single entries.  The row is summed in at most kVerifyUnits units, a wave each;
 // the sums' own cumulative sum names the unit where the goal is passed, and
-// only that unit is read again.  One launch sums the units, a second one picks
-// (a single workgroup a sequence for both was no faster for 32000 entries and
-// twice as slow for 262144; nothing has to be cleared between calls).
+// only that unit is read again.  One launch sums the units, a second one picks;
+// nothing has to be cleared between calls.  One sequence: 6.3 us from a graph for
+// 32000 and 6.8 for 262144 entries, a chain of about five dependent loads and
+// two launches (a single workgroup for all of it took 15 and 31; 1024 threads
+// that pick instead of 256, 14).  256 sequences x 3 drafts x 131071 bf16: 21 us
+// for the sums (5.3 TB/s of the rows that matter) and 5 to pick.
 #include "gdn.h"
 #include "gdn_elem.hpp"
 #include "gdn_launch.hpp"
@@ -23,7 +26,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kT = 1024;                     // threads of the picking workgroup, K at most
+constexpr int kT = 256;                      // threads of a workgroup
 
 // Negative, infinite and NaN entries count as 0.
 __device__ __forceinline__ double weight(float p) {
@@ -212,15 +215,11 @@ template <typename PT>
 __device__ __forceinline__ void pick(const VerifyArgs &a, int64_t b, const Row &row, int unit,
                                      double *sums) {
     __shared__ double totals[2][kT / 64];
-    __shared__ int at, last;
+    __shared__ int hits[kT / 64], ends[kT / 64];          // a wave's first entry past the goal, its last live one
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const float u_sample = a.u_sample[b];
-    const int drafted = tid < a.K ? a.draft_tokens[b * a.K + tid] : -1;   // K <= kT
+    const int drafted = tid < a.K ? a.draft_tokens[b * a.K + tid] : -1;
     Weights<PT> w(a, b, row);
-    if (tid == 0) {
-        at = a.V;
-        last = -1;
-    }
     // every wave finds the unit by itself: four sums a lane
     constexpr int S = kVerifyUnits / 64;
     double x[S], run, total;
@@ -268,9 +267,9 @@ __device__ __forceinline__ void pick(const VerifyArgs &a, int64_t b, const Row &
         u = __builtin_amdgcn_readlane(end, l);
         base = lane_of(end_base, l);
     }
-    __syncthreads();                                      // at and last are set
+    int token = -1;
     if (u >= 0) {
-        int found = a.V;
+        int found = -1;
         end = -1;
         for (int i = 0, turn = 0; i < unit; i += 4 * kT, turn ^= 1) {
             const int64_t v = static_cast<int64_t>(u) * unit + i + tid * 4;
@@ -292,17 +291,35 @@ __device__ __forceinline__ void pick(const VerifyArgs &a, int64_t b, const Row &
                 c += z[j];
                 if (z[j] > 0.0) {
                     end = static_cast<int>(first + j);
-                    if (c > goal) found = min(found, end);
+                    if (c > goal && found < 0) found = end;
                 }
             }
+            // entries lie in the order of lanes, waves and turns
+            const unsigned long long h = __ballot(found >= 0), e = __ballot(end >= 0);
+            const int first_hit = h ? __builtin_amdgcn_readlane(found, __ffsll(h) - 1) : -1;
+            const int last_end = e ? __builtin_amdgcn_readlane(end, 63 - __clzll(e)) : -1;
+            if (i > 0) __syncthreads();                   // the turn before is read
+            if (lane == 0) {
+                hits[wave] = first_hit;
+                ends[wave] = last_end;
+            }
+            __syncthreads();
+            int hit_now = -1;
+#pragma unroll
+            for (int k = kT / 64 - 1; k >= 0; --k) hit_now = hits[k] >= 0 ? hits[k] : hit_now;
+#pragma unroll
+            for (int k = 0; k < kT / 64; ++k) token = ends[k] >= 0 ? ends[k] : token;
+            if (hit_now >= 0) {
+                token = hit_now;
+                break;
+            }
+            found = end = -1;
         }
-        if (found < a.V) atomicMin(&at, found);
-        if (end >= 0) atomicMax(&last, end);
-        __syncthreads();
     }
-    const int token = u < 0 ? -1 : at < a.V ? at : last;
     int32_t *out = a.tokens + b * (a.K + 1);
     if (tid < a.K) out[tid] = tid < row.accepted ? drafted : tid == row.accepted ? token : -1;
+    for (int i = tid + kT; i < a.K; i += kT)
+        out[i] = i < row.accepted ? a.draft_tokens[b * a.K + i] : i == row.accepted ? token : -1;
     if (tid == 0) {
         out[a.K] = row.accepted == a.K ? token : -1;
         a.accepted[b] = row.accepted;
@@ -311,7 +328,7 @@ __device__ __forceinline__ void pick(const VerifyArgs &a, int64_t b, const Row &
 
 // The units' sums, a wave each, and the decision, for k_verify_pick.
 template <typename PT>
-__global__ __launch_bounds__(256) void k_verify_sums(VerifyArgs a, int unit, int units) {
+__global__ __launch_bounds__(kT) void k_verify_sums(VerifyArgs a, int unit, int units) {
     const int64_t b = blockIdx.y;
     const Row row = decide<PT>(a, b);
     const Weights<PT> w(a, b, row);
@@ -333,7 +350,8 @@ __global__ __launch_bounds__(kT) void k_verify_pick(VerifyArgs a, int unit, int 
     const int tid = threadIdx.x;
     const int32_t *r = a.rows + b * 4;
     const Row row{r[0], r[1], r[2]};
-    if (tid < kVerifyUnits) sums[tid] = tid < units ? a.partial[b * kVerifyUnits + tid] : 0.0;
+    static_assert(kVerifyUnits == kT, "");
+    sums[tid] = tid < units ? a.partial[b * kVerifyUnits + tid] : 0.0;
     __syncthreads();
     pick<PT>(a, b, row, unit, sums);
 }
@@ -349,7 +367,7 @@ hipError_t launch(const VerifyArgs &a, hipStream_t s) {
     // a wave per unit, or about 2048 workgroups in all (1024 to 8192 within 5 %)
     const int most = (2048 + a.B - 1) / a.B;
     const unsigned wide = static_cast<unsigned>(min((units + 3) / 4, most));
-    k_verify_sums<PT><<<dim3(wide, static_cast<unsigned>(a.B)), dim3(256), 0, s>>>(a, unit, units);
+    k_verify_sums<PT><<<dim3(wide, static_cast<unsigned>(a.B)), dim3(kT), 0, s>>>(a, unit, units);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     k_verify_pick<PT><<<dim3(static_cast<unsigned>(a.B)), dim3(kT), 0, s>>>(a, unit, units);
