@@ -571,7 +571,11 @@ __global__ __launch_bounds__(64 * WN * WM) void k_linear_block(LinearArgs a, int
 // this loop runs at 2.5, at 8192 x 8192 x 8192 the whole product at 2.3 and at
 // 32768 x 12352 x 2048 into bf16 at 1.9, where the results' bytes weigh more.
 // 32 x 32 x 32 instructions measured 25 % slower, blocks of 64 k in four
-// buffers 10 %.  kRagged: k is not a multiple of 256.
+// buffers 10 %.
+// kRagged: k is not a multiple of 256.  Its masks do not fit beside operands
+// held ahead (139 us at 4096 x 8192 x 2176 into bf16, most of it spilt
+// registers), so it fetches one block ahead and reads a half when it multiplies
+// it: 94 us there, and 7 % slower than the other loop where that one is right.
 struct Tile {
     int n, m;
 };
@@ -656,10 +660,10 @@ __global__ __launch_bounds__(512) void k_linear_tile(LinearArgs a, int tiles_n, 
     };
     const int left = a.K - last * kBK - 16 * g;           // of the last block, from this lane's chunk on
     auto mul = [&](int half, int b) {
-        if constexpr (kRagged) {                          // tokens' bytes past the last are zero
+        if constexpr (kRagged) {                          // weights' bytes past the last are zero
             const bool z = b > last || (b == last && 64 * half >= left);
 #pragma unroll
-            for (int j = 0; j < TM; ++j) xf[half][j] = z ? i4{0, 0, 0, 0} : xf[half][j];
+            for (int i = 0; i < TN; ++i) wf[half][i] = z ? i4{0, 0, 0, 0} : wf[half][i];
         }
 #pragma unroll
         for (int i = 0; i < TN; ++i)
@@ -667,22 +671,32 @@ __global__ __launch_bounds__(512) void k_linear_tile(LinearArgs a, int tiles_n, 
             for (int j = 0; j < TM; ++j)
                 acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[half][i], xf[half][j], acc[i][j], 0, 0, 0);
     };
-    // block b is in cur, its first half in registers, the next block on its way to nxt
     auto block = [&](int8_t *cur, int8_t *nxt, int b) {
-        read(cur, 1);
-        mul(0, b);
-        wait_mem<0, true>();
-        barrier();                                        // nxt has landed, cur is read
-        fetch(cur);
-        read(nxt, 0);
-        mul(1, b);
+        if constexpr (kRagged) {                          // block b is in cur, nxt is free
+            fetch(nxt);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                read(cur, half);
+                mul(half, b);
+            }
+            wait_mem<0, true>();
+            barrier();                                    // nxt has landed, cur is read
+        } else {                                          // and its first half in registers, the next on its way
+            read(cur, 1);
+            mul(0, b);
+            wait_mem<0, true>();
+            barrier();
+            fetch(cur);
+            read(nxt, 0);
+            mul(1, b);
+        }
     };
     aim();
     fetch(b0);
-    fetch(b1);
+    if constexpr (!kRagged) fetch(b1);
     wait_mem<0, true>();
     barrier();
-    read(b0, 0);
+    if constexpr (!kRagged) read(b0, 0);
     for (;;) {
         aim();
 #pragma unroll
