@@ -360,7 +360,8 @@ int gdn_layer_tail_noalloc(const gdn_dims *dims, const gdn_tail_params *params, 
 /*
  * gdn_add_rmsnorm_q8 - residual addition, RMS norm and 8-bit codes of `rows`
  * rows of n elements:
- *   h = x + residual rounded to the residual's type (h = x without one),
+ *   h = x + residual, added in binary32 and rounded to the residual's type
+ *       (h = x without one),
  *   g_i = h_i * norm_w[i],  G = max_i |g_i|,
  *   q_i = rint(127 * g_i / G) (ties to even),
  *   scale = G / 127 / sqrt(mean(h^2) + eps),

@@ -125,6 +125,24 @@ def test_rows_with_nothing_left(g, V):
     check(g, c)
 
 
+@pytest.mark.parametrize("dtype,step", [(torch.float32, 2.0 ** -149), (torch.bfloat16, 2.0 ** -133),
+                                        (torch.float16, 2.0 ** -24)])
+def test_subnormal_probabilities(g, dtype, step):
+    """Whole multiples of the type's smallest value: products, differences and
+    sums are exact in binary64, so nothing may be flushed to zero."""
+    print(f"\n  verify: subnormal probabilities {dtype}", flush=True)
+    gen = torch.Generator().manual_seed(11)
+    B, K, V = 24, 2, 777
+    target = (torch.randint(0, 4, (B, K + 1, V), generator=gen).double() * step).to(dtype)
+    draft = (torch.randint(0, 4, (B, K, V), generator=gen).double() * step).to(dtype)
+    assert float(target.double().max()) == 3 * step
+    c = dict(target=target, draft=draft,
+             draft_tokens=torch.randint(0, V, (B, K), generator=gen).int(),
+             u_accept=torch.rand(B, K, generator=gen), u_sample=torch.rand(B, generator=gen))
+    a, t = check(g, c)
+    assert 0 < a.sum() < B * K and (t[np.arange(B), a] >= 0).all()
+
+
 def test_peaked_rows(g):
     """Rows where one entry holds nearly everything, at every place of a vector and
     of a unit, so that the goal falls next to it."""
