@@ -231,16 +231,16 @@ __device__ __forceinline__ void write_tile(const LinearArgs &a, int c0, int m0, 
     }
 }
 
-// The channel and token tile of workgroup id.  From 8 channel tiles on, the
-// token tiles of one follow each other on one XCD (ids modulo 8), whose L2 then
-// holds their weights; ids past the last tile have tn >= tiles_n.
+// The channel and token tile of workgroup id.  Each XCD (ids modulo 8) takes a
+// run of consecutive tiles, the token tiles of a channel tile after each other,
+// so that its L2 holds their weights; ids past the last tile have tn >= tiles_n.
 __device__ __forceinline__ void tile_of(int id, int tiles_n, int tiles_m, int &tn, int &tm) {
-    const int q = id >> 3;
-    tn = tiles_n < 8 ? id % tiles_n : (q / tiles_m) * 8 + (id & 7);
-    tm = tiles_n < 8 ? id / tiles_n : q % tiles_m;
+    const int t = (id & 7) * static_cast<int>(gridDim.x >> 3) + (id >> 3);
+    tn = t / tiles_m;
+    tm = t - tn * tiles_m;
 }
 inline dim3 tile_grid(int64_t tiles_n, int64_t tiles_m) {
-    return dim3(static_cast<unsigned>((tiles_n < 8 ? tiles_n : (tiles_n + 7) / 8 * 8) * tiles_m));
+    return dim3(static_cast<unsigned>((tiles_n * tiles_m + 7) / 8 * 8));
 }
 
 // ------------------------------------------------------------- split product
@@ -729,11 +729,13 @@ hipError_t launch_ring(const LinearArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <typename OT, int BN, int BM, int WN, int WM, int S>
+template <typename OT, int BN, int BM, int WN, int WM, int S, bool kAligned = false>
 hipError_t launch_block(const LinearArgs &a, hipStream_t s) {
     const int tn = static_cast<int>(tiles(a.N, BN)), tm = static_cast<int>(tiles(a.M, BM));
     const dim3 block(64 * WN * WM);
-    if (a.K % 16 == 0)
+    if constexpr (kAligned)                               // called for rows of whole chunks only
+        k_linear_block<OT, BN, BM, WN, WM, S, true><<<tile_grid(tn, tm), block, 0, s>>>(a, tn, tm);
+    else if (a.K % 16 == 0)
         k_linear_block<OT, BN, BM, WN, WM, S, true><<<tile_grid(tn, tm), block, 0, s>>>(a, tn, tm);
     else
         k_linear_block<OT, BN, BM, WN, WM, 2, false><<<tile_grid(tn, tm), block, 0, s>>>(a, tn, tm);
@@ -763,12 +765,28 @@ hipError_t launch(const LinearArgs &a, hipStream_t s) {
     // 12.8 | 14.4 at 128 x 2048, 12.5 | 13.3 | 15.8 at 512 x 2048, 55 | 37 | 29
     // at 512 x 12352).
     const int cus = device_cus();
+    const auto wide = [&](int bn, int bm) { return (bn <= 64 || bn < 2 * a.N) && (bm <= 16 || bm < 2 * a.M); };
     const auto fits = [&](int bn, int bm) {
-        return (bn <= 64 || bn < 2 * a.N) && (bm <= 16 || bm < 2 * a.M) &&
-               4 * tiles(a.N, bn) * tiles(a.M, bm) >= 3 * static_cast<int64_t>(cus);
+        return wide(bn, bm) && 4 * tiles(a.N, bn) * tiles(a.M, bm) >= 3 * static_cast<int64_t>(cus);
     };
-    if (fits(256, 256) && a.K % 16 == 0) return launch_tile<OT>(a, cus, s);
-    if (fits(128, 128)) return launch_block<OT, 128, 128, 2, 4, 4>(a, s);
+    if (fits(128, 128)) {
+        // From here on a compute unit holds one workgroup, and the tile whose rounds
+        // of workgroups end first is taken: ns a round of 4096 k, of no k, measured
+        // (us, 128 x 128 | 256 x 128 | 256 x 256 tiles: 29 | 23 | 36 at 512 x 12352,
+        // 33 | 24 | 37 at 640, 77 for the last at 2048, k = 2048).  The choice was the
+        // fastest or within 10 % from 300 to 32768 tokens.
+        const auto ns = [&](int bn, int bm, int k4096, int none) {
+            const int64_t rounds = (tiles(a.N, bn) * tiles(a.M, bm) + cus - 1) / cus;
+            return wide(bn, bm) ? rounds * (static_cast<int64_t>(a.K) * k4096 / 4096 + none) : INT64_MAX;
+        };
+        const int64_t small = ns(128, 128, 16800, 6100);
+        if (a.K % 16 == 0) {
+            const int64_t mid = ns(256, 128, 33600, 6200), large = ns(256, 256, 54500, 8700);
+            if (large <= mid && large <= small) return launch_tile<OT>(a, cus, s);
+            if (mid <= small) return launch_block<OT, 256, 128, 4, 2, 3, true>(a, s);
+        }
+        return launch_block<OT, 128, 128, 2, 4, 4>(a, s);
+    }
     if (fits(64, 128)) return launch_block<OT, 64, 128, 2, 2, 4>(a, s);
     if (fits(64, 64)) return launch_ring<4, 4, 4, 2>(a, s);
     if (fits(32, 64)) return launch_ring<2, 4, 4, 3>(a, s);

@@ -89,6 +89,18 @@ def test_every_kernel_over_types(g, M, splits, K, dtype):
     check(g, M, splits, K, dtype, True, full=True)
 
 
+# One round of 128 x 128 tiles, one and several rounds of 256 x 128, rounds of
+# 256 x 256, and tile counts that do not divide among the XCDs.
+ROUNDS = [(1500, [1025, 1025]), (1290, [2000, 500, 13]), (640, [8192, 4096, 64]), (4100, [5000]),
+          (300, [12352]), (130, [8300])]
+
+
+@pytest.mark.parametrize("K", [16, 128, 240, 256, 384, 512, 656, 2064])
+@pytest.mark.parametrize("M,splits", ROUNDS)
+def test_rounds_of_tiles(g, M, splits, K):
+    check(g, M, splits, K, torch.float32 if K % 256 else torch.bfloat16, K < 300)
+
+
 @pytest.mark.parametrize("M,N,K", [(40000, 5, 200), (3, 40000, 33), (9000, 17, 64), (5000, 5000, 48)])
 def test_narrow_and_wide(g, M, N, K):
     check(g, M, [N], K, torch.float32, False)
