@@ -297,6 +297,13 @@ __global__ __launch_bounds__(64 * WK) void k_linear_ring(LinearArgs a, int tiles
                 xf[h][j] = *reinterpret_cast<const i4 *>(piece + (TN + j) * 2048 + rd[h]);
         }
     };
+    // Weights past the last k are zero; `left` of k from this lane's chunk on.
+    auto mask = [&](int left) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < TN; ++i) wf[h][i] = 64 * h < left ? wf[h][i] : i4{0, 0, 0, 0};
+    };
     auto mul = [&]() {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -309,8 +316,11 @@ __global__ __launch_bounds__(64 * WK) void k_linear_ring(LinearArgs a, int tiles
     int8_t *const p0 = r0 + wave * kPiece, *const p1 = r1 + wave * kPiece;
     if constexpr (kVec) {
         int8_t *const p2 = S > 2 ? r2 + wave * kPiece : nullptr, *const p3 = S > 3 ? r3 + wave * kPiece : nullptr;
+        // the block past the whole ones, if there is one and it is this wave's
+        const bool part = full * kBK < a.K && wave == full % WK;
+        const int all = n + (part ? 1 : 0);
         auto fetch = [&](int8_t *piece, int i) {          // past the end: the last block again
-            const int k0 = (wave + min(i, n - 1) * WK) * kBK;
+            const int k0 = (wave + min(i, all - 1) * WK) * kBK;
 #pragma unroll
             for (int j = 0; j < L; ++j)
                 fetch16(piece + j * 1024, j < 2 * TN ? pw : px, j < 2 * TN ? nw : nx, off[j], k0);
@@ -322,7 +332,7 @@ __global__ __launch_bounds__(64 * WK) void k_linear_ring(LinearArgs a, int tiles
             fetch(piece, i + S);
             mul();
         };
-        if (n > 0) {
+        if (all > 0) {
             fetch(p0, 0);
             fetch(p1, 1);
             if constexpr (S > 2) fetch(p2, 2);
@@ -348,6 +358,12 @@ __global__ __launch_bounds__(64 * WK) void k_linear_ring(LinearArgs a, int tiles
         }
         // the last fetches have landed before LDS takes the sums or ends
         wait_mem<0, true>();
+        if (part) {
+            const int slot = n % S;
+            read(slot == 0 ? p0 : slot == 1 ? p1 : slot == 2 ? p2 : p3);
+            mask(a.K - full * kBK - 16 * g);
+            mul();
+        }
     } else {
         i4 v[L];
         auto load = [&](int i) {
@@ -364,7 +380,7 @@ __global__ __launch_bounds__(64 * WK) void k_linear_ring(LinearArgs a, int tiles
             mul();
         }
     }
-    if (full * kBK < a.K && wave == full % WK) {          // the bytes past the last whole block
+    if (!kVec && full * kBK < a.K && wave == full % WK) { // the bytes past the last whole block
         for (int k = full * kBK; k < a.K; k += 64) {
 #pragma unroll
             for (int i = 0; i < TN; ++i)
@@ -460,8 +476,9 @@ __global__ __launch_bounds__(64 * WN * WM) void k_linear_block(LinearArgs a, int
     // piece j of this wave in a buffer
     auto at = [&](int j) { return (j < LN ? 0 : BN * kBK) + ((j < LN ? j : j - LN) * NW + wave) * 1024; };
     if constexpr (kVec) {
+        const int all = (a.K + kBK - 1) / kBK;            // with the block past the whole ones
         auto fetch = [&](int8_t *buf, int i) {            // past the end: the last block again
-            const int k0 = min(i, n - 1) * kBK;
+            const int k0 = min(i, all - 1) * kBK;
 #pragma unroll
             for (int j = 0; j < L; ++j) fetch16(buf + at(j), j < LN ? pw : px, j < LN ? nw : nx, off[j], k0);
         };
@@ -475,11 +492,11 @@ __global__ __launch_bounds__(64 * WN * WM) void k_linear_block(LinearArgs a, int
             read(nxt, 0);
             mul(1);
         };
+        fetch(r0, 0);
+        fetch(r1, 1);
+        if constexpr (S > 2) fetch(r2, 2);
+        if constexpr (S > 3) fetch(r3, 3);
         if (n > 0) {
-            fetch(r0, 0);
-            fetch(r1, 1);
-            if constexpr (S > 2) fetch(r2, 2);
-            if constexpr (S > 3) fetch(r3, 3);
             wait_mem<(S - 1) * L, true>();
             barrier();
             read(r0, 0);
@@ -542,7 +559,20 @@ __global__ __launch_bounds__(64 * WN * WM) void k_linear_block(LinearArgs a, int
     // the last fetches have landed, and every wave is done with the ring
     wait_mem<0, true>();
     __syncthreads();
-    if (n * kBK < a.K) {                                  // the bytes past the last whole block
+    if (kVec && n * kBK < a.K) {                          // the block past the whole ones
+        const int slot = n % S, left = a.K - n * kBK - 16 * g;
+        const int8_t *buf = slot == 0 ? r0 : slot == 1 ? r1 : slot == 2 ? r2 : r3;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            read(buf, half);
+#pragma unroll
+            for (int i = 0; i < TN; ++i)                  // weights past the last k are zero
+                wf[half][i] = 64 * half < left ? wf[half][i] : i4{0, 0, 0, 0};
+            mul(half);
+        }
+        __syncthreads();
+    }
+    if (!kVec && n * kBK < a.K) {                         // the bytes past the last whole block
 #pragma unroll 1
         for (int j = wave; j < (BN + BM) / 8; j += NW) {
             const int row = j * 8 + (lane >> 3), in = row < BN ? row : row - BN;
@@ -572,10 +602,9 @@ __global__ __launch_bounds__(64 * WN * WM) void k_linear_block(LinearArgs a, int
 // 32768 x 12352 x 2048 into bf16 at 1.9, where the results' bytes weigh more.
 // 32 x 32 x 32 instructions measured 25 % slower, blocks of 64 k in four
 // buffers 10 %.
-// kRagged: k is not a multiple of 256.  Its masks do not fit beside operands
-// held ahead (139 us at 4096 x 8192 x 2176 into bf16, most of it spilt
-// registers), so it fetches one block ahead and reads a half when it multiplies
-// it: 94 us there, and 7 % slower than the other loop where that one is right.
+// k is a multiple of 256 here: masks for a ragged k did not fit beside operands
+// held ahead, and one half at a time was 15-75 % slower than rounds of 256 x 128
+// tiles (124 us against 89 at 4096 x 8192 x 2176 into f32).
 struct Tile {
     int n, m;
 };
@@ -590,7 +619,7 @@ __device__ __forceinline__ Tile tile_at(int i, int tiles_n, int tiles_m) {
     return Tile{__builtin_amdgcn_readfirstlane(n), __builtin_amdgcn_readfirstlane(grp * kG + in - n * gm)};
 }
 
-template <typename OT, bool kRagged>
+template <typename OT>
 __global__ __launch_bounds__(512) void k_linear_tile(LinearArgs a, int tiles_n, int tiles_m) {
     constexpr int BN = 256, BM = 256, WN = 4, NW = 8;
     constexpr int TN = BN / WN / 16, TM = BM / (NW / WN) / 16;
@@ -601,8 +630,7 @@ __global__ __launch_bounds__(512) void k_linear_tile(LinearArgs a, int tiles_n, 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
     const int wn = wave % WN, wm = wave / WN;
-    const int blocks = (a.K + kBK - 1) / kBK, last = blocks - 1;
-    const int even = (blocks + 1) & ~1;                   // blocks of a tile, in pairs
+    const int blocks = a.K / kBK;                         // of a tile, in pairs
     const int tiles = tiles_n * tiles_m;
 
     // each XCD (ids modulo 8) takes a run of consecutive tiles
@@ -635,12 +663,12 @@ __global__ __launch_bounds__(512) void k_linear_tile(LinearArgs a, int tiles_n, 
         nxn = span(a.M - f.m * BM, a.K);
     };
     auto fetch = [&](int8_t *buf) {
-        const int k0 = (kRagged ? min(fb, last) : fb) * kBK;
+        const int k0 = fb * kBK;
 #pragma unroll
         for (int j = 0; j < F; ++j) fetch16(buf + (j * NW + wave) * 1024, pw, nw, off[j], k0);
 #pragma unroll
         for (int j = 0; j < F; ++j) fetch16(buf + BN * kBK + (j * NW + wave) * 1024, px, nx, off[j], k0);
-        const bool wrap = ++fb == even;                   // at most once a tile
+        const bool wrap = ++fb == blocks;                  // at most once a tile
         fb = wrap ? 0 : fb;
         ft = wrap ? ftn : ft;
         pw = wrap ? pwn : pw;
@@ -658,54 +686,38 @@ __global__ __launch_bounds__(512) void k_linear_tile(LinearArgs a, int tiles_n, 
         for (int i = 0; i < TN; ++i)
             wf[half][i] = *reinterpret_cast<const i4 *>(buf + (wn * TN + i) * 16 * kBK + rd[half]);
     };
-    const int left = a.K - last * kBK - 16 * g;           // of the last block, from this lane's chunk on
-    auto mul = [&](int half, int b) {
-        if constexpr (kRagged) {                          // weights' bytes past the last are zero
-            const bool z = b > last || (b == last && 64 * half >= left);
-#pragma unroll
-            for (int i = 0; i < TN; ++i) wf[half][i] = z ? i4{0, 0, 0, 0} : wf[half][i];
-        }
+    auto mul = [&](int half) {
 #pragma unroll
         for (int i = 0; i < TN; ++i)
 #pragma unroll
             for (int j = 0; j < TM; ++j)
                 acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[half][i], xf[half][j], acc[i][j], 0, 0, 0);
     };
-    auto block = [&](int8_t *cur, int8_t *nxt, int b) {
-        if constexpr (kRagged) {                          // block b is in cur, nxt is free
-            fetch(nxt);
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                read(cur, half);
-                mul(half, b);
-            }
-            wait_mem<0, true>();
-            barrier();                                    // nxt has landed, cur is read
-        } else {                                          // and its first half in registers, the next on its way
-            read(cur, 1);
-            mul(0, b);
-            wait_mem<0, true>();
-            barrier();
-            fetch(cur);
-            read(nxt, 0);
-            mul(1, b);
-        }
+    // a block is in cur, its first half in registers, the next block on its way to nxt
+    auto block = [&](int8_t *cur, int8_t *nxt) {
+        read(cur, 1);
+        mul(0);
+        wait_mem<0, true>();
+        barrier();                                        // nxt has landed, cur is read
+        fetch(cur);
+        read(nxt, 0);
+        mul(1);
     };
     aim();
     fetch(b0);
-    if constexpr (!kRagged) fetch(b1);
+    fetch(b1);
     wait_mem<0, true>();
     barrier();
-    if constexpr (!kRagged) read(b0, 0);
+    read(b0, 0);
     for (;;) {
         aim();
 #pragma unroll
         for (int i = 0; i < TN; ++i)
 #pragma unroll
             for (int j = 0; j < TM; ++j) acc[i][j] = i4{0, 0, 0, 0};
-        for (int b = 0; b < even; b += 2) {
-            block(b0, b1, b);
-            block(b1, b0, b + 1);
+        for (int b = 0; b < blocks; b += 2) {
+            block(b0, b1);
+            block(b1, b0);
         }
         write_tile<OT, TN, TM>(a, t.n * BN + wn * TN * 16, t.m * BM + wm * TM * 16, lane,
                                stage + wave * kStageBytes, acc);
@@ -747,10 +759,7 @@ hipError_t launch_tile(const LinearArgs &a, int cus, hipStream_t s) {
     const int tn = static_cast<int>(tiles(a.N, 256)), tm = static_cast<int>(tiles(a.M, 256));
     const int64_t all = static_cast<int64_t>(tn) * tm, most = cus >= 8 ? cus / 8 * 8 : 8;
     const dim3 grid(static_cast<unsigned>(all < most ? (all + 7) / 8 * 8 : most));
-    if (a.K % (2 * kBK) == 0)
-        k_linear_tile<OT, false><<<grid, dim3(512), 0, s>>>(a, tn, tm);
-    else
-        k_linear_tile<OT, true><<<grid, dim3(512), 0, s>>>(a, tn, tm);
+    k_linear_tile<OT><<<grid, dim3(512), 0, s>>>(a, tn, tm);
     return hipGetLastError();
 }
 
@@ -781,7 +790,8 @@ hipError_t launch(const LinearArgs &a, hipStream_t s) {
         };
         const int64_t small = ns(128, 128, 16800, 6100);
         if (a.K % 16 == 0) {
-            const int64_t mid = ns(256, 128, 33600, 6200), large = ns(256, 256, 54500, 8700);
+            const int64_t mid = ns(256, 128, 33600, 6200), 
+                          large = a.K % 256 == 0 ? ns(256, 256, 54500, 8700) : INT64_MAX;
             if (large <= mid && large <= small) return launch_tile<OT>(a, cus, s);
             if (mid <= small) return launch_block<OT, 256, 128, 4, 2, 3, true>(a, s);
         }
