@@ -34,12 +34,24 @@ constexpr int kBK = 128;      // bytes of k in a block: one line of a row
 // spread over all banks (no conflict counted).
 __device__ __forceinline__ int swz(int row) { return row & 7; }
 
-// Sixteen bytes at k of a row of K bytes, zero past its end.
-__device__ __forceinline__ i4 load16(const int8_t *row, int k, int K) {
+// Sixteen bytes at any address.
+__device__ __forceinline__ i4 any16(const int8_t *p) {
+    typedef int32_t any __attribute__((ext_vector_type(4), aligned(1)));
+    return *reinterpret_cast<const any *>(p);
+}
+
+// Sixteen bytes at k of a row of K bytes, zero past its end.  The load may reach
+// into the next rows, but not past the end of the matrix.
+__device__ __forceinline__ i4 load16(const int8_t *row, int k, int K, const int8_t *end) {
     i4 v = {0, 0, 0, 0};
-    if (k + 16 <= K) {
-        typedef int32_t any __attribute__((ext_vector_type(4), aligned(1)));
-        v = *reinterpret_cast<const any *>(row + k);
+    if (k >= K) return v;
+    if (row + k + 16 <= end) {
+        v = any16(row + k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = K - k - 4 * i;                  // bytes of this word that are the row's
+            v[i] = n >= 4 ? v[i] : n <= 0 ? 0 : v[i] & ((1 << 8 * n) - 1);
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -48,12 +60,6 @@ __device__ __forceinline__ i4 load16(const int8_t *row, int k, int K) {
                                                  << (8 * (i % 4)));
     }
     return v;
-}
-
-// Sixteen bytes at any address.
-__device__ __forceinline__ i4 any16(const int8_t *p) {
-    typedef int32_t any __attribute__((ext_vector_type(4), aligned(1)));
-    return *reinterpret_cast<const any *>(p);
 }
 
 // 1 KiB straight into LDS from the `bytes` bytes at base: lane l's 16 bytes at
@@ -106,6 +112,7 @@ struct Channels {
     int32_t live;       // how many of the four belong to it
     float scale[4], bias[4];
 
+    Channels() = default;
     __device__ __forceinline__ Channels(const LinearArgs &a, int c, size_t bytes) {
         int first;
         const int s = group_of(a, c, first);
@@ -381,13 +388,14 @@ __global__ __launch_bounds__(64 * WK) void k_linear_ring(LinearArgs a, int tiles
         }
     }
     if (!kVec && full * kBK < a.K && wave == full % WK) { // the bytes past the last whole block
+        const int8_t *const we = a.w + static_cast<int64_t>(a.N) * a.K, *const xe = a.a + static_cast<int64_t>(a.M) * a.K;
         for (int k = full * kBK; k < a.K; k += 64) {
 #pragma unroll
             for (int i = 0; i < TN; ++i)
-                wf[0][i] = load16(a.w + static_cast<int64_t>(min(c0 + 16 * i + r, a.N - 1)) * a.K, k + 16 * g, a.K);
+                wf[0][i] = load16(a.w + static_cast<int64_t>(min(c0 + 16 * i + r, a.N - 1)) * a.K, k + 16 * g, a.K, we);
 #pragma unroll
             for (int j = 0; j < TM; ++j)
-                xf[0][j] = load16(a.a + static_cast<int64_t>(min(m0 + 16 * j + r, a.M - 1)) * a.K, k + 16 * g, a.K);
+                xf[0][j] = load16(a.a + static_cast<int64_t>(min(m0 + 16 * j + r, a.M - 1)) * a.K, k + 16 * g, a.K, xe);
 #pragma unroll
             for (int i = 0; i < TN; ++i)
 #pragma unroll
@@ -403,19 +411,28 @@ __global__ __launch_bounds__(64 * WK) void k_linear_ring(LinearArgs a, int tiles
     for (int t = 0; t < TN * TM; ++t)
         *reinterpret_cast<i4 *>((t < kIn0 ? p0 + t * 1024 : p1 + (t - kIn0) * 1024) + lane * 16) =
             acc[t / TM][t % TM];
+    constexpr int NT = (TN * TM + WK - 1) / WK;           // tiles a wave sums and writes: wave, wave + WK, ..
+    Channels chs[NT];
+    float sas[NT];
+    chs[0] = ch;
+    sas[0] = sa;
+#pragma unroll
+    for (int i = 1; i < NT; ++i) {
+        const int t = min(wave + i * WK, TN * TM - 1);
+        chs[i] = Channels(a, min(c0 + 16 * (t / TM) + 4 * g, a.N - 1), type_bytes(a));
+        sas[i] = a.a_scale[min(m0 + 16 * (t % TM) + r, a.M - 1)];
+    }
     __syncthreads();
-    for (int t = wave; t < TN * TM; t += WK) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const int t = wave + i * WK;
+        if (t >= TN * TM) break;
         const int8_t *p = t < kIn0 ? r0 + t * 1024 : r1 + (t - kIn0) * 1024;
         i4 s = *reinterpret_cast<const i4 *>(p + lane * 16);
 #pragma unroll
         for (int k = 1; k < WK; ++k) s += *reinterpret_cast<const i4 *>(p + k * kPiece + lane * 16);
-        if (t == wave) {
-            if (c < a.N && m < a.M) put4(a, ch, c, m, sa, s);
-        } else {
-            const int ct = c0 + 16 * (t / TM) + 4 * g, mt = m0 + 16 * (t % TM) + r;
-            if (ct < a.N && mt < a.M)
-                put4(a, Channels(a, ct, type_bytes(a)), ct, mt, a.a_scale[mt], s);
-        }
+        const int ct = c0 + 16 * (t / TM) + 4 * g, mt = m0 + 16 * (t % TM) + r;
+        if (ct < a.N && mt < a.M) put4(a, chs[i], ct, mt, sas[i], s);
     }
 }
 
@@ -578,8 +595,9 @@ __global__ __launch_bounds__(64 * WN * WM) void k_linear_block(LinearArgs a, int
             const int row = j * 8 + (lane >> 3), in = row < BN ? row : row - BN;
             const int8_t *p = row < BN ? a.w + static_cast<int64_t>(min(c0 + in, a.N - 1)) * a.K
                                        : a.a + static_cast<int64_t>(min(m0 + in, a.M - 1)) * a.K;
+            const int8_t *end = row < BN ? a.w + static_cast<int64_t>(a.N) * a.K : a.a + static_cast<int64_t>(a.M) * a.K;
             *reinterpret_cast<i4 *>(r0 + j * 1024 + lane * 16) =
-                load16(p, n * kBK + 16 * ((lane & 7) ^ swz(in)), a.K);
+                load16(p, n * kBK + 16 * ((lane & 7) ^ swz(in)), a.K, end);
         }
         __syncthreads();
         read(r0, 0);
@@ -765,22 +783,28 @@ hipError_t launch_tile(const LinearArgs &a, int cus, hipStream_t s) {
 
 template <typename OT>
 hipError_t launch(const LinearArgs &a, hipStream_t s) {
-    // The largest tile that still gives three of four compute units a workgroup,
-    // and is no wider than the operands rounded up (64 channels, 16 tokens at
-    // least).  Measured over 1..2048 tokens x (2048 channels, k = 4096 | 12352,
-    // k = 2048), f32 out: the tile this picks was the fastest or within 5 %,
-    // but 13 % slower than a 64 x 128 tile at 64 x 12352; one size larger or
-    // smaller cost up to 2x (us, 64 x 64 | 64 x 128 | 128 x 128 tiles: 10.8 |
-    // 12.8 | 14.4 at 128 x 2048, 12.5 | 13.3 | 15.8 at 512 x 2048, 55 | 37 | 29
-    // at 512 x 12352).
+    // The largest tile that still gives more than half of the compute units a
+    // workgroup, and is no wider than the operands rounded up (64 channels, 16
+    // tokens at least): each holds one of most kernels here, so the next smaller
+    // tile would take two rounds.  Measured over 1..2048 tokens x (2048 channels,
+    // k = 4096 | 12352, k = 2048), f32 out: the tile this picks was the fastest or
+    // within 5 %, but 13 % slower than a 64 x 128 tile at 64 x 12352; one size
+    // larger or smaller cost up to 2x (us, 64 x 64 | 64 x 128 | 128 x 128 tiles:
+    // 10.8 | 12.8 | 14.4 at 128 x 2048, 12.5 | 13.3 | 15.8 at 512 x 2048, 55 | 37 |
+    // 29 at 512 x 12352), and asking for three of four units up to 2.2x (320 x
+    // 2048, k = 4096: 15.2 | 11.3; 5953 x 144, k = 64: 9.7 | 4.4).
     const int cus = device_cus();
     const auto wide = [&](int bn, int bm) { return (bn <= 64 || bn < 2 * a.N) && (bm <= 16 || bm < 2 * a.M); };
     const auto fits = [&](int bn, int bm) {
-        return wide(bn, bm) && 4 * tiles(a.N, bn) * tiles(a.M, bm) >= 3 * static_cast<int64_t>(cus);
+        return wide(bn, bm) && 2 * tiles(a.N, bn) * tiles(a.M, bm) > static_cast<int64_t>(cus);
     };
     if (fits(128, 128)) {
-        // From here on a compute unit holds one workgroup, and the tile whose rounds
-        // of workgroups end first is taken: ns a round of 4096 k, of no k, measured
+        // A short k leaves little to hide latency behind but another workgroup, so
+        // two buffers and two workgroups a unit (5000 x 5000, k = 64, f32: 21.7 us
+        // against 26.3 for what follows; equal at k = 256).
+        if (a.K < 256 && a.K % 16 == 0) return launch_block<OT, 128, 128, 2, 4, 2, true>(a, s);
+        // Else a unit holds one workgroup, and the tile whose rounds of workgroups end
+        // first is taken: ns a round of 4096 k, of no k, measured
         // (us, 128 x 128 | 256 x 128 | 256 x 256 tiles: 29 | 23 | 36 at 512 x 12352,
         // 33 | 24 | 37 at 640, 77 for the last at 2048, k = 2048).  The choice was the
         // fastest or within 10 % from 300 to 32768 tokens.
@@ -790,7 +814,7 @@ hipError_t launch(const LinearArgs &a, hipStream_t s) {
         };
         const int64_t small = ns(128, 128, 16800, 6100);
         if (a.K % 16 == 0) {
-            const int64_t mid = ns(256, 128, 33600, 6200), 
+            const int64_t mid = ns(256, 128, 33600, 6200),
                           large = a.K % 256 == 0 ? ns(256, 256, 54500, 8700) : INT64_MAX;
             if (large <= mid && large <= small) return launch_tile<OT>(a, cus, s);
             if (mid <= small) return launch_block<OT, 256, 128, 4, 2, 3, true>(a, s);

@@ -101,6 +101,32 @@ def test_rounds_of_tiles(g, M, splits, K):
     check(g, M, splits, K, torch.float32 if K % 256 else torch.bfloat16, K < 300)
 
 
+# Just enough tiles for each kernel, from 16 x 16 to one round and more of 256 x
+# 256, with k of no, one and several blocks, whole and not.
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+@pytest.mark.parametrize("K", [48, 256, 400, 512, 768, 1040, 1280])
+@pytest.mark.parametrize("M,splits", [(13, [2000]), (13, [8300]), (30, [4100, 55]), (30, [8300]), (200, [1203]),
+                                      (190, [3000]), (500, [2000, 100]), (1200, [1801]), (4100, [2500, 2477])])
+def test_smallest_of_each_kernel(g, dtype, M, splits, K):
+    check(g, M, splits, K, dtype, K % 512 == 0)
+
+
+# k that is no multiple of 16: the bytes past a row's end belong to the next row,
+# or lie past the matrix behind the last one.
+@pytest.mark.parametrize("K", [1, 3, 7, 13, 18, 31, 47, 111, 127, 129, 143, 250, 391])
+@pytest.mark.parametrize("M,splits", [(1, [1]), (2, [3]), (17, [100]), (320, [2048]), (700, [82, 429, 26]),
+                                      (1500, [1000]), (5953, [144])])
+def test_rows_that_end_anywhere(g, M, splits, K):
+    check(g, M, splits, K, torch.float32, K % 2 == 1, full=True)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("M,splits,K", [(5953, [144], 64), (10729, [80], 64), (3000, [1000, 1999, 1], 192),
+                                        (1500, [2050], 240), (320, [2048], 400), (640, [2047], 272)])
+def test_short_inner_lengths(g, dtype, M, splits, K):
+    check(g, M, splits, K, dtype, True)
+
+
 @pytest.mark.parametrize("M,N,K", [(40000, 5, 200), (3, 40000, 33), (9000, 17, 64), (5000, 5000, 48)])
 def test_narrow_and_wide(g, M, N, K):
     check(g, M, [N], K, torch.float32, False)
