@@ -64,7 +64,7 @@ __device__ __forceinline__ V reduce(V x, V *red, F join) {
     x = join(x, dpp<0x4E>(x));
     x = join(x, dpp<0x141>(x));
     x = join(x, dpp<0x140>(x));
-    x = join(join(lane(x, 0), lane(x, 16)), join(lane(x, 32), lane(x, 48)));
+    if constexpr (T > 16) x = join(join(lane(x, 0), lane(x, 16)), join(lane(x, 32), lane(x, 48)));
     if constexpr (T > 64) {
         if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
         __syncthreads();
@@ -245,23 +245,25 @@ struct RowOf {
     }
 };
 
-// T threads per row (R rows a workgroup, so R = 1 or T = 64), the row in
-// registers: CH chunks a thread.  Rows of ordinary magnitude are worked in
+// T threads per row (R rows a workgroup, so R = 1 or T = 16 or 64), the row in
+// registers: CH chunks a thread.  512 threads are held to four waves a SIMD, so
+// that a compute unit holds two rows (10000 x 4100 f32: 66 us against 113).  Rows of ordinary magnitude are worked in
 // binary32 where that is exact enough and in binary64 where it is not: binary64
 // throughout is right too, but 20 such operations an element bound the kernel
 // (32768 x 2048 bf16 with a residual: 129 us against 86).
 template <typename XT, typename RT, bool kNorm, int T, int CH, int R>
-__global__ __launch_bounds__(T * R) void k_quant_row(QuantArgs a) {
+__global__ __launch_bounds__(T * R, T == 512 ? 4 : 1) void k_quant_row(QuantArgs a) {
     constexpr int V = chunk_of<XT, RT>();
     typedef RowOf<XT, RT, kNorm, V> Row;
     typedef RowOf<XT, RT, kNorm, 1> One;
-    static_assert(R == 1 || T == 64, "");
-    __shared__ uint32_t red_m[T / 64];
-    __shared__ double red_s[T / 64], red_t[T / 64], red_u[T / 64];
+    static_assert(R == 1 || T == 64 || T == 16, "");
+    constexpr int W = (T + 63) / 64;                      // a row's waves
+    __shared__ uint32_t red_m[W];
+    __shared__ double red_s[W], red_t[W], red_u[W];
     __shared__ unsigned long long exact[R];
     const int tid = threadIdx.x % T;
     const int64_t id = static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / T;
-    if (id >= a.rows) return;                             // whole waves; no barrier if R > 1
+    if (id >= a.rows) return;                             // whole rows of lanes; no barrier if R > 1
     if (kNorm && tid == 0) exact[threadIdx.x / T] = 0;    // joined behind the first reduction's barrier
     const Row row(a, id);
     // the elements past the last whole chunk, one a thread
@@ -362,13 +364,18 @@ template <typename XT, typename RT, bool kNorm>
 hipError_t launch(const QuantArgs &a, hipStream_t s) {
     // Threads a row by its length alone, so a row's bits do not depend on how many
     // there are; 8 or 16 elements a thread (32 without a norm, with one they leave
-    // two waves a SIMD: 10000 x 6001 f16 with a residual 207 us for 175).  us on 100000 x 512 f32: a wave a row 116, 256
-    // threads a row 197; on 32768 x 2048 bf16 with a residual: 256 threads 86, a
-    // wave a row 196.
+    // two waves a SIMD: 10000 x 6001 f16 with a residual 207 us for 175).  us on
+    // 100000 rows: 16 lanes a row 23 at 100 bf16 with a residual and 36 at 256, a
+    // wave a row 65 and 60; 116 at 512 f32, 256 threads a row 197.  On 32768 x 2048
+    // bf16 with a residual: 256 threads 86, a wave a row 196.
     const unsigned rows = static_cast<unsigned>(a.rows);
     constexpr int V = chunk_of<XT, RT>(), C8 = 8 / V, C16 = 16 / V;
     const int body = a.n - a.n % V;
-    if (body <= 512)
+    if (body <= 128)
+        k_quant_row<XT, RT, kNorm, 16, C8, 16><<<dim3((rows + 15) / 16), dim3(256), 0, s>>>(a);
+    else if (body <= 256)
+        k_quant_row<XT, RT, kNorm, 16, C16, 16><<<dim3((rows + 15) / 16), dim3(256), 0, s>>>(a);
+    else if (body <= 512)
         k_quant_row<XT, RT, kNorm, 64, C8, 4><<<dim3((rows + 3) / 4), dim3(256), 0, s>>>(a);
     else if (body <= 1024)
         k_quant_row<XT, RT, kNorm, 64, C16, 4><<<dim3((rows + 3) / 4), dim3(256), 0, s>>>(a);
