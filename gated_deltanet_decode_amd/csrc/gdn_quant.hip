@@ -363,8 +363,9 @@ __global__ __launch_bounds__(1024) void k_quant_long(QuantArgs a) {
 template <typename XT, typename RT, bool kNorm>
 hipError_t launch(const QuantArgs &a, hipStream_t s) {
     // Threads a row by its length alone, so a row's bits do not depend on how many
-    // there are; 8 or 16 elements a thread (32 without a norm, with one they leave
-    // two waves a SIMD: 10000 x 6001 f16 with a residual 207 us for 175).  us on
+    // there are; 8 or 16 elements a thread, 32 in long rows without a norm (1600 x
+    // 16000 bf16 22 us for 26; with a norm their registers leave too few waves: 10000
+    // x 6001 f16 with a residual 207 us for 175).  us on
     // 100000 rows: 16 lanes a row 23 at 100 bf16 with a residual and 36 at 256, a
     // wave a row 65 and 60; 116 at 512 f32, 256 threads a row 197.  On 32768 x 2048
     // bf16 with a residual: 256 threads 86, a wave a row 196.
@@ -387,7 +388,8 @@ hipError_t launch(const QuantArgs &a, hipStream_t s) {
         k_quant_row<XT, RT, kNorm, kNorm ? 512 : 256, kNorm ? C16 : 2 * C16, 1>
             <<<dim3(rows), dim3(kNorm ? 512 : 256), 0, s>>>(a);
     else if (body <= 16384)
-        k_quant_row<XT, RT, kNorm, 1024, C16, 1><<<dim3(rows), dim3(1024), 0, s>>>(a);
+        k_quant_row<XT, RT, kNorm, kNorm ? 1024 : 512, kNorm ? C16 : 2 * C16, 1>
+            <<<dim3(rows), dim3(kNorm ? 1024 : 512), 0, s>>>(a);
     else
         k_quant_long<XT, RT, kNorm><<<dim3(rows), dim3(1024), 0, s>>>(a);
     return hipGetLastError();

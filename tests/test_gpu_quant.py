@@ -145,6 +145,16 @@ def test_narrow_rows(g, xt, rt, n):
         check_quant(g, x)
 
 
+@pytest.mark.parametrize("t", list(sr.TYPES))
+@pytest.mark.parametrize("n", [4100, 8192, 8199, 8200, 8201, 12345, 16384, 16391, 16392])
+def test_quantize_long_rows(g, t, n):
+    print(f"\n  quantize_q8 {t} n={n}", flush=True)
+    x = make(9, n, sr.TYPES[t], 22)
+    x[4] *= 1e-30 if t != "f16" else 1e-6
+    x[6, n - 1] = float("inf")
+    check_quant(g, x)
+
+
 @pytest.mark.parametrize("n", [16, 100, 2048, 4099, 20000])
 def test_ties_go_to_even(g, n):
     """127 g / 254 = g / 2 is a tie for every odd g."""
