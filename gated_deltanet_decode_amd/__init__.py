@@ -124,6 +124,8 @@ class LinearOut(ctypes.Structure):
 
 
 LINEAR_MAX_OUTS = 4
+_GROUPS = [LinearOut * n for n in range(LINEAR_MAX_OUTS + 1)]
+_OUTS = [f"outs[{i}]" for i in range(LINEAR_MAX_OUTS)]
 
 lib.gdn_add_rmsnorm_q8.restype = ctypes.c_int
 lib.gdn_add_rmsnorm_q8.argtypes = [_i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, ctypes.c_float,
@@ -428,6 +430,7 @@ try:
 except NameError:
     _TYPES, _I8, _I32 = {}, None, None
 _NO_TYPE = -1
+_INT32_MAX = 2 ** 31 - 1
 
 
 def _addr(t, name, dtype, shape, device):
@@ -467,6 +470,8 @@ def _lead(t, name, ndim, types=None):
         _typed(t, name, types)
     if t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dimensions, got shape {tuple(t.shape)}")
+    if t.numel() > _INT32_MAX and max(t.shape) > _INT32_MAX:    # the C arguments are int32
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, no dimension may pass {_INT32_MAX}")
     return t.get_device()
 
 
@@ -535,14 +540,16 @@ def linear_q8(a, a_scale, w, w_scale, outs, bias=None, stream=None) -> None:
         raise ValueError(f"outs must be 1 to {LINEAR_MAX_OUTS} tensors, got {len(outs)}")
     _lead(outs[0], "outs[0]", 2, _TYPES)
     dtype = outs[0].dtype
-    groups = (LinearOut * len(outs))()
+    addrs = []
     N = 0
     for i, o in enumerate(outs):
-        _lead(o, f"outs[{i}]", 2, _TYPES)
+        name = _OUTS[i]
+        if i:
+            _lead(o, name, 2, _TYPES)
         n = o.shape[1]
-        groups[i].out = _addr(o, f"outs[{i}]", dtype, (M, n), dev)
-        groups[i].n = n
+        addrs.append((_addr(o, name, dtype, (M, n), dev), n))
         N += n
+    groups = _GROUPS[len(outs)](*addrs)
     _issue(lib.gdn_linear_q8,
            (M, K, _addr(a, "a", _I8, (M, K), dev), _addr(a_scale, "a_scale", _F32, (M,), dev),
             _addr(w, "w", _I8, (N, K), dev), _addr(w_scale, "w_scale", _F32, (N,), dev),
@@ -598,6 +605,8 @@ def pair_commit(accepted, state, state_next, conv_state=None, conv_state_next=No
         _lead(conv_state, "conv_state", len(lead) + 2)
         rs = lead + tuple(conv_state.shape[len(lead):])
         ring = rs[-1] * rs[-2]
+        if ring > _INT32_MAX:
+            raise ValueError(f"conv_state holds {ring} floats a sequence, at most {_INT32_MAX}")
     d = Dims(Hv, Hv, dk, dv)           # the copy does not depend on the key heads
     _issue(lib.gdn_pair_commit,
            (ctypes.byref(d), layers, B, _addr(accepted, "accepted", _I32, (B,), dev),

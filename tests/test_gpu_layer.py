@@ -240,3 +240,30 @@ def test_messages_stay_with_their_call(g):
     g.quantize_q8(x, q, s)
     torch.cuda.synchronize()
     assert g.last_error() == "" and int(q.abs().max()) == 127
+
+
+def test_sizes_past_32_bits_are_refused(g):
+    """The C arguments are 32 bits wide: a dimension that would wrap around to a
+    small one (here of expanded tensors, that take no memory) is refused."""
+    wide = 2 ** 32 + 3
+    one = lambda dtype, *s: torch.zeros(*[1] * len(s), dtype=dtype, device="cuda").expand(*s)
+    v = torch.zeros(3, device="cuda")
+    i8 = torch.int8
+    for shape in ((wide, 2), (2, wide)):
+        with pytest.raises(ValueError, match="no dimension may pass"):
+            g.quantize_q8(one(torch.float16, *shape), one(i8, *shape), v)
+        with pytest.raises(ValueError, match="no dimension may pass"):
+            g.add_rmsnorm_q8(one(torch.float32, *shape), None, None, v, one(i8, *shape), v)
+        with pytest.raises(ValueError, match="no dimension may pass"):
+            g.linear_q8(one(i8, *shape), v, one(i8, 3, 2), v, one(torch.float32, 2, 3))
+    with pytest.raises(ValueError, match="no dimension may pass"):
+        g.linear_q8(one(i8, 2, 16), v, one(i8, wide + 2, 16), v,
+                    [torch.zeros(2, 2, device="cuda"), one(torch.float32, 2, wide)])
+    i32 = torch.zeros(2, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="no dimension may pass"):
+        g.verify(one(torch.float32, 1, 2, wide), None, i32[:1].view(1, 1), v[:1].view(1, 1), v[:1], i32[:1],
+                 i32.view(1, 2), workspace=torch.empty(4096, dtype=torch.uint8, device="cuda"))
+    state = torch.zeros(1, 1, 128, 128, device="cuda")
+    ring = one(torch.float32, 1, 2 ** 16, 2 ** 16 + 4)
+    with pytest.raises(ValueError, match="floats a sequence"):
+        g.pair_commit(i32[:1], state, state.clone(), ring, ring)
