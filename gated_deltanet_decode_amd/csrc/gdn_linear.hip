@@ -785,8 +785,8 @@ template <typename OT>
 hipError_t launch(const LinearArgs &a, hipStream_t s) {
     // The largest tile that still gives more than half of the compute units a
     // workgroup, and is no wider than the operands rounded up (64 channels, 16
-    // tokens at least): each holds one of most kernels here, so the next smaller
-    // tile would take two rounds.  Measured over 1..2048 tokens x (2048 channels,
+    // tokens at least): a unit holds one workgroup of most kernels here, so the next
+    // smaller tile would take two rounds.  Measured over 1..2048 tokens x (2048 channels,
     // k = 4096 | 12352, k = 2048), f32 out: the tile this picks was the fastest or
     // within 5 %, but 13 % slower than a 64 x 128 tile at 64 x 12352; one size
     // larger or smaller cost up to 2x (us, 64 x 64 | 64 x 128 | 128 x 128 tiles:
