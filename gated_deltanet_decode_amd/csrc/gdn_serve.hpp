@@ -73,7 +73,7 @@ struct CommitArgs {
     const float *ring_next;
     int32_t layers;
     int32_t B;
-    int32_t state_f4;                // float4s of one sequence's state in one layer
+    int64_t state_f4;                // float4s of one sequence's state in one layer
     int32_t ring_f4;
 };
 

@@ -297,7 +297,7 @@ int gdn_pair_commit(const gdn_dims *dims, int32_t layers, int32_t B, const int32
     a.ring_next = conv_state_next;
     a.layers = layers;
     a.B = B;
-    a.state_f4 = static_cast<int32_t>(sf / 4);
+    a.state_f4 = sf / 4;                  // past 2^31 from 524288 heads on
     a.ring_f4 = conv_floats / 4;
     (void)hipGetLastError();
     return hip_status(gdn::launch_commit(a, static_cast<hipStream_t>(stream)),
