@@ -5,10 +5,10 @@
 // r = 1 / sqrt(mean(h^2) + eps), the normed row is y_i = r g_i and its codes
 // are rint(127 y_i / max|y|).  r cancels: q_i = rint(127 g_i / G), and only the
 // scale r G / 127 needs it.  h and w are binary32, so g_i is exact in binary64
-// and a code depends on nothing but the row's own products; the quotient is
-// formed as g_i * (127 / G), at most 4e-14 off, and a value that close to a
-// border is divided out (so ties are those of the formula).  The sum of
-// squares is kept in binary64 too.
+// and a code depends on nothing but the row's own products.  The quotient is
+// formed as g_i (127 / G), in binary32 for rows of ordinary magnitude (at most
+// 3.1e-5 off) and in binary64 for the others and for long rows (4e-14); a value
+// that close to a border is settled by an exact comparison, ties included.
 #include "gdn.h"
 #include "gdn_elem.hpp"
 #include "gdn_serve.hpp"
@@ -23,13 +23,31 @@ struct NoType {
 constexpr double kRound = 6755399441055744.0;             // 1.5 * 2^52
 constexpr float kRound32 = 12582912.0f;                   // 1.5 * 2^23
 
+// The code of a product whose quotient t = 127 g / top, known to 4e-5, lies near a
+// border k + 1/2 (k = floor(|t|)): 254 |g| against (2 k + 1) top, exactly.  g and
+// top are products of two 24-bit numbers, multiples of units u and v with
+// |g| < 2^48 u and top < 2^48 v; next to a border 256 |g| - (2 k + 1) top is about
+// 2 |g| <= 2 top, and so below 2^50 times the smaller unit: the fused step and the
+// subtraction after it are exact.  127 g alone takes up to 55 bits, so a rounded
+// quotient is not enough here.  It is without a norm, where g and top have 24 bits:
+// 127 g is exact, and a quotient that is no tie is 2^-33 or more off one (20001 x
+// 4097 bf16 40 us for 42 with the comparison).
+template <bool kNorm>
+__device__ __forceinline__ uint32_t settled(double g, double top) {
+    if constexpr (!kNorm) return static_cast<uint32_t>(__builtin_bit_cast(uint64_t, 127.0 * g / top + kRound));
+    const double a = fabs(g), k = floor(127.0 * a / top);
+    const double past = fma(-(2.0 * k + 1.0), top, 256.0 * a) - 2.0 * a;
+    const int n = static_cast<int>(k), q = past > 0.0 ? n + 1 : past < 0.0 ? n : n + (n & 1);
+    return static_cast<uint32_t>(g < 0.0 ? -q : q);
+}
+
 // One code, as the low byte of a word, in binary64: t = g * (127 / G) is within
-// 4e-14 of 127 g / G, and a value that near a border is divided out.  Adding
-// 1.5 * 2^52 rounds t to an integer, ties to even, and leaves it in the low word.
+// 4e-14 of 127 g / G, and a value that near a border is settled.  Adding 1.5 * 2^52
+// rounds t to an integer, ties to even, and leaves it in the low word.
+template <bool kNorm>
 __device__ __forceinline__ uint32_t code(double g, double inv, double top) {
-    const double t = g * inv;
-    double s = t + kRound;
-    if (fabs(t - (s - kRound)) > 0.5 - 1e-12) s = 127.0 * g / top + kRound;
+    const double t = g * inv, s = t + kRound;
+    if (fabs(t - (s - kRound)) > 0.5 - 1e-12) return settled<kNorm>(g, top);
     return static_cast<uint32_t>(__builtin_bit_cast(uint64_t, s));
 }
 
@@ -214,12 +232,12 @@ struct RowOf {
                                           double top) const {
         uint32_t b[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) b[j] = inv == 0.0 ? 0u : code(product(c, h, j), inv, top);
+        for (int j = 0; j < V; ++j) b[j] = inv == 0.0 ? 0u : code<kNorm>(product(c, h, j), inv, top);
         put(b, i);
     }
     // The same codes from binary32: product, top, reciprocal and the last product
     // each round, so t is within 127 * 4 * 2^-24 = 3.1e-5 of 127 g / G; what lies
-    // within 4e-5 of a border is divided out in binary64.
+    // within 4e-5 of a border is settled in binary64.
     __device__ __forceinline__ void codes32(const Chunk &c, const float (&h)[V], int i, float inv,
                                             double top) const {
         uint32_t b[V];
@@ -237,7 +255,7 @@ struct RowOf {
             double g = 0.0;
 #pragma unroll
             for (int j = 0; j < V; ++j) g = j == k ? product(c, h, j) : g;
-            const uint32_t e = static_cast<uint32_t>(__builtin_bit_cast(uint64_t, 127.0 * g / top + kRound));
+            const uint32_t e = settled<kNorm>(g, top);
 #pragma unroll
             for (int j = 0; j < V; ++j) b[j] = j == k ? e : b[j];
         }
