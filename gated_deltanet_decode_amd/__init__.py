@@ -558,6 +558,8 @@ def linear_q8(a, a_scale, w, w_scale, outs, bias=None, stream=None) -> None:
 
 
 def verify_workspace_bytes(B: int, V: int) -> int:
+    if not (0 < B <= _INT32_MAX and 0 < V <= _INT32_MAX):     # the C arguments are int32
+        return 0
     return int(lib.gdn_verify_workspace_bytes(B, V))
 
 
