@@ -1,7 +1,7 @@
 // gdn_elem.hpp - device-side element types of the operators around the
 // recurrent branch: conversions to and from binary32, vector accesses at any
-// element's alignment, and the sums over a wave.  Included by kernel sources
-// only.
+// element's alignment, and moves between a wave's lanes.  Included by kernel
+// sources only.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -51,16 +51,25 @@ struct Pack {
     static __device__ __forceinline__ void store(B *p, vec v) { *reinterpret_cast<any *>(p) = v; }
 };
 
-// Sum and maximum over the 64 lanes; every lane gets the same bits.
-__device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off, 64);
-    return x;
+// Moves of values between a wave's lanes: by DPP control within rows of 16 lanes
+// (0 where there is no source lane), and one lane's value to all.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t x) {
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), CTRL, 0xF, 0xF, false));
 }
-__device__ __forceinline__ double wave_max(double x) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) x = fmax(x, __shfl_xor(x, off, 64));
-    return x;
+template <int CTRL>
+__device__ __forceinline__ double dpp(double x) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(dpp<CTRL>(static_cast<uint32_t>(b >> 32))) << 32 |
+                                          dpp<CTRL>(static_cast<uint32_t>(b)));
+}
+__device__ __forceinline__ uint32_t lane_of(uint32_t x, int l) {
+    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x), l));
+}
+__device__ __forceinline__ double lane_of(double x, int l) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(lane_of(static_cast<uint32_t>(b >> 32), l)) << 32 |
+                                          lane_of(static_cast<uint32_t>(b), l));
 }
 
 }  // namespace

@@ -59,31 +59,13 @@ __device__ __forceinline__ uint32_t magnitude(float x) {  // orders as |x|, infi
 // Reductions over a row's T threads; every thread gets the same bits.  Within
 // sixteen lanes by DPP (xor 1, xor 2, mirrors of 8 and 16), then over the wave's
 // four rows of lanes, then over the waves through `red` (a value each).
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t x) {
-    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), CTRL, 0xF, 0xF, false));
-}
-template <int CTRL>
-__device__ __forceinline__ double dpp(double x) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, x);
-    return __builtin_bit_cast(double, static_cast<uint64_t>(dpp<CTRL>(static_cast<uint32_t>(b >> 32))) << 32 |
-                                          dpp<CTRL>(static_cast<uint32_t>(b)));
-}
-__device__ __forceinline__ uint32_t lane(uint32_t x, int l) {
-    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x), l));
-}
-__device__ __forceinline__ double lane(double x, int l) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, x);
-    return __builtin_bit_cast(double, static_cast<uint64_t>(lane(static_cast<uint32_t>(b >> 32), l)) << 32 |
-                                          lane(static_cast<uint32_t>(b), l));
-}
 template <int T, typename V, typename F>
 __device__ __forceinline__ V reduce(V x, V *red, F join) {
     x = join(x, dpp<0xB1>(x));
     x = join(x, dpp<0x4E>(x));
     x = join(x, dpp<0x141>(x));
     x = join(x, dpp<0x140>(x));
-    if constexpr (T > 16) x = join(join(lane(x, 0), lane(x, 16)), join(lane(x, 32), lane(x, 48)));
+    if constexpr (T > 16) x = join(join(lane_of(x, 0), lane_of(x, 16)), join(lane_of(x, 32), lane_of(x, 48)));
     if constexpr (T > 64) {
         if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
         __syncthreads();

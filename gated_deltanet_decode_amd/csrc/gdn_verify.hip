@@ -142,22 +142,8 @@ struct Weights {
     }
 };
 
-// Within a wave by DPP: moves of a lane's value inside rows of 16 lanes, then
-// the rows' sums by lane reads.
-template <int CTRL>
-__device__ __forceinline__ double dpp(double x) {         // 0 where there is no source lane
-    const uint64_t b = __builtin_bit_cast(uint64_t, x);
-    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), CTRL, 0xF, 0xF, false);
-    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), CTRL, 0xF, 0xF, false);
-    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
-}
-__device__ __forceinline__ double lane_of(double x, int l) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, x);
-    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b), l);
-    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), l);
-    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
-}
-// Inclusive sums over the wave's lanes, and the total.
+// Inclusive sums over the wave's lanes, and the total: within rows of 16 lanes by
+// DPP, then the rows' sums by lane reads.
 __device__ __forceinline__ double scan(double x, double &total) {
     x += dpp<0x111>(x);                                   // row_shr 1, 2, 4, 8
     x += dpp<0x112>(x);
@@ -223,7 +209,7 @@ __device__ __forceinline__ void pick(const VerifyArgs &a, int64_t b, const Row &
     // every wave finds the unit by itself: four sums a lane
     constexpr int S = kVerifyUnits / 64;
     double x[S], run, total;
-    for (int turn = 0;; ++turn) {
+    for (;;) {
         double own = 0.0;
 #pragma unroll
         for (int j = 0; j < S; ++j) {
@@ -294,11 +280,11 @@ __device__ __forceinline__ void pick(const VerifyArgs &a, int64_t b, const Row &
                     if (c > goal && found < 0) found = end;
                 }
             }
-            // entries lie in the order of lanes, waves and turns
+            // entries lie in the order of lanes, waves and turns; the barrier above is
+            // behind every read of the turn before
             const unsigned long long h = __ballot(found >= 0), e = __ballot(end >= 0);
             const int first_hit = h ? __builtin_amdgcn_readlane(found, __ffsll(h) - 1) : -1;
             const int last_end = e ? __builtin_amdgcn_readlane(end, 63 - __clzll(e)) : -1;
-            if (i > 0) __syncthreads();                   // the turn before is read
             if (lane == 0) {
                 hits[wave] = first_hit;
                 ends[wave] = last_end;
