@@ -593,7 +593,9 @@ def pair_commit(accepted, state, state_next, conv_state=None, conv_state_next=No
     """gdn_pair_commit: accepted [B] int32; state and state_next [B][Hv][dv][dk]
     (or [layers][B][Hv][dv][dk]) and, optionally, conv_state and
     conv_state_next [B][K-1][C] (or [layers][B][K-1][C]): the tentative
-    buffers of the sequences with accepted >= 1 replace the committed ones."""
+    buffers of the sequences with accepted >= 1 replace the committed ones.  A
+    pair holds one drafted position: accepted is that of a verify of one draft
+    a sequence."""
     if getattr(state, "ndim", 5) == 4:
         dev, layers, sh = _lead(state, "state", 4), 1, tuple(state.shape)
         lead = sh[:1]

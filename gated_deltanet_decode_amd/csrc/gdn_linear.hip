@@ -9,7 +9,7 @@
 // of row r (channels from w as the first operand, tokens from a as the second)
 // and receives channels 4 g..4 g+3 of token r.
 //
-// Kernels, by how many tokens there are:
+// Kernels, by how many tiles the product has (launch() says which):
 //   k_linear_ring   a workgroup's waves split k over one small tile
 //   k_linear_block  one tile a workgroup, its waves share the operands in LDS
 //   k_linear_tile   persistent workgroups over 256 x 256 tiles
@@ -615,7 +615,7 @@ __global__ __launch_bounds__(64 * WN * WM) void k_linear_block(LinearArgs a, int
 // of one block, and the waves' pieces for the stores).  The fetches run two
 // blocks ahead of the multiplication and over tile borders, so the next tile is
 // on its way while this one is written.  Matrix instructions alone reach 3.5
-// PFLOP/s here on random operands (the clock drops under them); per block of k
+// POP/s here on random operands (the clock drops under them); per block of k
 // this loop runs at 2.5, at 8192 x 8192 x 8192 the whole product at 2.3 and at
 // 32768 x 12352 x 2048 into bf16 at 1.9, where the results' bytes weigh more.
 // 32 x 32 x 32 instructions measured 25 % slower, blocks of 64 k in four

@@ -358,7 +358,7 @@ hipError_t launch(const QuantArgs &a, hipStream_t s) {
     // Threads a row by its length alone, so a row's bits do not depend on how many
     // there are; 8 or 16 elements a thread, 32 in long rows without a norm (1600 x
     // 16000 bf16 22 us for 26; with a norm their registers leave too few waves: 10000
-    // x 6001 f16 with a residual 207 us for 175).  us on
+    // x 6001 f16 with a residual 131 us for 110, 3000 x 12000 bf16 288 for 66).  us on
     // 100000 rows: 16 lanes a row 23 at 100 bf16 with a residual and 36 at 256, a
     // wave a row 65 and 60; 116 at 512 f32, 256 threads a row 197.  On 32768 x 2048
     // bf16 with a residual: 256 threads 86, a wave a row 196.

@@ -5,8 +5,13 @@
 // are and u q_i(d) < p_i(d); the token after the accepted run is drawn by
 // inverting the cumulative sum of w = max(p - q, 0) at the refusal (or of p
 // when no draft is left).  Probabilities of at most 24 significant bits make
-// the product exact in binary64 and the sums good to 1e-16 of the total, so
-// the outcome is the formula's whatever the order of the sums.
+// the product exact in binary64, and with it what is accepted.  The sums round:
+// a lane's 16 or 32 terms (V / 16384 of a large V), the scans over lanes, units
+// and entries, and scans less their own term: at most 80 + V / 16384 roundings of
+// 2^-53 of the total on a path.  The token is the definition's unless the goal
+// lies that close to a cumulative sum; then it may be another entry with a weight
+// and a sum as close (where the unit's entries, summed in another order than the
+// units, do not pass the goal, the unit's last one with a weight).
 //
 // Only one row of the target and at most one of the draft matter to a
 // sequence, once the run of accepted tokens is known, and that takes 2 K
@@ -16,8 +21,11 @@
 // nothing has to be cleared between calls.  One sequence: 6.3 us from a graph for
 // 32000 and 6.8 for 262144 entries, a chain of about five dependent loads and
 // two launches (a single workgroup for all of it took 15 and 31; 1024 threads
-// that pick instead of 256, 14).  256 sequences x 3 drafts x 131071 bf16: 21 us
-// for the sums (5.3 TB/s of the rows that matter) and 5 to pick.
+// that pick instead of 256, 14).  256 sequences x 3 drafts x 131071 bf16: 20 us
+// for the sums and 5 to pick; the rows that matter come at 4.5 TB/s sampled
+// (91 MB) and 3.3 greedy (67 MB), and the vector units are busy 63 and 73 % of
+// that time: the binary64 conversions and sums of each entry weigh more than
+// memory.
 #include "gdn.h"
 #include "gdn_elem.hpp"
 #include "gdn_launch.hpp"

@@ -348,9 +348,9 @@ int gdn_layer_tail_noalloc(const gdn_dims *dims, const gdn_tail_params *params, 
  * accepted, and the states that move with it).  One decoded layer is
  *   gdn_add_rmsnorm_q8 -> gdn_linear_q8 (x | z | ba) -> gdn_gate_transform,
  *   gdn_layer_tail or gdn_layer_tail_pair -> gdn_quantize_q8 -> gdn_linear_q8.
- * None of these calls needs the head geometry.  They follow the conventions
- * above; element types are named by the codes below (any other code:
- * GDN_ERR_SHAPE).
+ * Of these only gdn_pair_commit needs the head geometry.  They follow the
+ * conventions above; element types are named by the codes below (any other
+ * code: GDN_ERR_SHAPE).
  */
 #define GDN_F32 0  /* IEEE binary32 */
 #define GDN_BF16 1 /* bfloat16      */
@@ -367,8 +367,10 @@ int gdn_layer_tail_noalloc(const gdn_dims *dims, const gdn_tail_params *params, 
  *   scale = G / 127 / sqrt(mean(h^2) + eps),
  * so q_i * scale is the normed row times the weight to half a step.  The
  * root mean square divides out of the codes: they depend on the products g_i
- * alone, which are formed and compared in binary64, so the codes are the
- * formula's exactly and do not depend on how the row is summed.  A row whose
+ * alone, which binary64 holds exactly, and a quotient next to a border is
+ * settled by an exact comparison, so the codes are the formula's, ties
+ * included, and do not depend on how the row is summed.  The sum of squares
+ * is binary64 and the scale rounds once to binary32.  A row whose
  * products are all zero gets q = 0 and scale = 0; a row with a NaN or an
  * infinity gets q = 0 and scale = NaN.
  *   x             [rows][n]  of x_type
@@ -435,7 +437,11 @@ int gdn_linear_q8(int32_t M, int32_t K, const int8_t *a, const float *a_scale, c
  *   the smallest v with w(v) > 0 and w(0) + .. + w(v) > u_sample[b] * sum(w),
  *   or the largest v with w(v) > 0 if there is none, or -1 if all are 0.
  * The accepted tokens and the drawn one follow p exactly when the drafts were
- * drawn from q.  Products, differences and sums are formed in binary64.
+ * drawn from q.  Products, differences and sums are formed in binary64: what
+ * is accepted is exact, and the drawn token is the definition's unless
+ * u_sample[b] * sum(w) lies within (80 + V / 16384) * 2^-53 * sum(w) of one of
+ * the sums w(0) + .. + w(v); then it may be another v with w(v) > 0 whose sum
+ * lies as close.
  * Rows need not sum to 1; entries that are negative or not finite count as 0.
  * A drafted token outside [0, V) is refused.
  *   target        [B][K+1][V]  of prob_type
@@ -468,7 +474,10 @@ size_t gdn_verify_workspace_bytes(int32_t B, int32_t V);
  * sequences whose draft was accepted: for every b with accepted[b] >= 1 and
  * every layer, state[b] = state_next[b] and conv_state[b] = conv_state_next[b];
  * the other sequences' buffers are not written (nor the tentative ones read).
- *   accepted         [B]  int32 (gdn_verify's)
+ * A pair holds one drafted position: `accepted` is that of a gdn_verify with
+ * K = 1.  After a K above 1 the state would stay one position behind for each
+ * draft accepted past the first.
+ *   accepted         [B]  int32
  *   state            [layers][B][n_v_heads][d_v][d_k]  in/out
  *   state_next       the same shape, read
  *   conv_state       [layers][B][conv_floats]  in/out, optional: NULL together
