@@ -141,9 +141,10 @@ def _prepare_rule(s, c, normal, uniform):
     else:
         s["out"] = torch.zeros(n, hv, D, dtype=t, device="cuda")
     if own and c["op"] != "decode":
-        size = _library().chunk_workspace_bytes if c["op"] == "chunk" else _library().chunk_backward_workspace_bytes
+        gdn = _library()
+        size = gdn.chunk_workspace_bytes if c["op"] == "chunk" else gdn.chunk_backward_workspace_bytes
         # the scratch a caller keeps from call to call
-        s["ws"] = torch.empty(size(c["b"], n, hv, hk), dtype=torch.uint8, device="cuda")
+        s["ws"] = torch.empty(size(c["b"], n, t, gdn.Dims(hv, hk, D, D)), dtype=torch.uint8, device="cuda")
 
 
 def prepare(case, seed):
