@@ -29,6 +29,10 @@ C entry points:
     verify_workspace_bytes(B, V)                 -> gdn_verify_workspace_bytes
     pair_commit(accepted, state, state_next, conv_state, conv_state_next)
                                                  -> gdn_pair_commit
+    chunk(q, k, v, beta, gate, out, state, state_out, offsets, slots, workspace)
+                                                 -> gdn_chunk
+    chunk_workspace_bytes(B, tokens, dtype)      -> gdn_chunk_workspace_bytes
+    decode(q, k, v, beta, gate, out, state, state_out, offsets, slots) -> gdn_decode
     last_error(), version()
 
 If the library has not been built, importing this package raises: there is
@@ -47,7 +51,8 @@ __all__ = ["GdnError", "Dims", "TailParams", "GateInputs", "lib", "step", "bind_
            "gate_transform",
            "layer_tail_ba",
            "layer_tail_ba_workspace_bytes", "add_rmsnorm_q8", "quantize_q8", "linear_q8",
-           "verify", "verify_workspace_bytes", "pair_commit", "last_error", "version", "PAGE_DIMS",
+           "verify", "verify_workspace_bytes", "pair_commit", "chunk", "chunk_workspace_bytes",
+           "decode", "last_error", "version", "PAGE_DIMS",
            "PAGE_TAIL", "ERRORS"]
 
 if not os.path.exists(LIBRARY):
@@ -141,6 +146,15 @@ lib.gdn_verify_workspace_bytes.restype = ctypes.c_size_t
 lib.gdn_verify_workspace_bytes.argtypes = [_i32, _i32]
 lib.gdn_pair_commit.restype = ctypes.c_int
 lib.gdn_pair_commit.argtypes = [_DP, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp]
+
+
+lib.gdn_chunk.restype = ctypes.c_int
+lib.gdn_chunk.argtypes = [_DP] + [_i32] * 3 + [_vp] * 7 + [_i32] + [_vp] * 3 + \
+    [_vp, ctypes.c_size_t, _vp]
+lib.gdn_chunk_workspace_bytes.restype = ctypes.c_size_t
+lib.gdn_chunk_workspace_bytes.argtypes = [_DP] + [_i32] * 3
+lib.gdn_decode.restype = ctypes.c_int
+lib.gdn_decode.argtypes = [_DP] + [_i32] * 3 + [_vp] * 7 + [_i32] + [_vp] * 3 + [_vp]
 
 
 class GdnError(RuntimeError):
@@ -619,3 +633,82 @@ def pair_commit(accepted, state, state_next, conv_state=None, conv_state_next=No
             None if rs is None else _addr(conv_state, "conv_state", _F32, rs, dev),
             None if rs is None else _addr(conv_state_next, "conv_state_next", _F32, rs, dev)),
            dev, stream)
+
+
+# ---------------------------------------------------------------------------
+# The delta rule over packed sequences, in several element types.
+def _packed(q, k, v, beta, gate, offsets):
+    """What the calls over packed sequences share: the GPU, dims, B, tokens, type
+    and the addresses of q, k, v, beta, gate and offsets.  With offsets q is
+    [tokens][Hk][dk], without them [B][T][Hk][dk] (v, beta and gate alike)."""
+    dev = _lead(q, "q", 4 if offsets is None else 3, _TYPES)
+    sh = tuple(q.shape)
+    lead, (Hk, dk) = sh[:-2], sh[-2:]
+    _lead(v, "v", len(sh), _TYPES)
+    Hv, dv = v.shape[-2:]
+    if offsets is None:
+        B, tokens = lead[0], lead[0] * lead[1]
+        if tokens > _INT32_MAX:
+            raise ValueError(f"q holds {tokens} tokens, at most {_INT32_MAX}")
+    else:
+        _lead(offsets, "offsets", 1)
+        B, tokens = offsets.shape[0] - 1, lead[0]
+    t = q.dtype
+    return dev, lead + (Hv, dv), Dims(Hv, Hk, dk, dv), (
+        B, tokens, _TYPES[t], _addr(q, "q", t, sh, dev), _addr(k, "k", t, sh, dev),
+        _addr(v, "v", t, lead + (Hv, dv), dev), _addr(beta, "beta", _F32, lead + (Hv,), dev),
+        _addr(gate, "gate", _F32, lead + (Hv,), dev),
+        None if offsets is None else _addr(offsets, "offsets", _I32, (B + 1,), dev))
+
+
+def _states(state, state_out, slots, B, dims, dev):
+    """slots, n_slots, state and state_out as the C calls take them."""
+    some = state if state is not None else state_out
+    n = B
+    if slots is not None:
+        if some is None:
+            raise ValueError("slots are given, but no state")
+        _lead(some, "state", 4)
+        n = some.shape[0]
+    sh = (n, dims.n_v_heads, dims.d_v, dims.d_k)
+    return (None if slots is None else _addr(slots, "slots", _I32, (B,), dev), n,
+            None if state is None else _addr(state, "state", _F32, sh, dev),
+            None if state_out is None else _addr(state_out, "state_out", _F32, sh, dev))
+
+
+def _scratch(workspace, dev):
+    ptr, size = _workspace(workspace)
+    if ptr is not None and workspace.get_device() != dev:
+        raise ValueError(f"workspace is on GPU {workspace.get_device()}, expected GPU {dev}")
+    return ptr, size
+
+
+def chunk_workspace_bytes(B: int, tokens: int, dtype, dims: Dims = PAGE_DIMS) -> int:
+    if dtype not in _TYPES or not (0 < B <= _INT32_MAX and 0 < tokens <= _INT32_MAX):
+        return 0
+    return int(lib.gdn_chunk_workspace_bytes(ctypes.byref(dims), B, tokens, _TYPES[dtype]))
+
+
+def chunk(q, k, v, beta, gate, out, state=None, state_out=None, offsets=None, slots=None,
+          workspace=None, stream=None) -> None:
+    """gdn_chunk: q, k [tokens][Hk][dk], v and out [tokens][Hv][dv] of float32,
+    bfloat16 or float16, beta and gate [tokens][Hv] float32, with offsets [B+1]
+    int32; or [B][T] in the place of [tokens] without offsets.  state (None:
+    zeros) and state_out (None: not wanted; may be state) [n_slots][Hv][dv][dk]
+    float32, slots [B] int32 or None (n_slots = B).  workspace: a GPU tensor of
+    at least chunk_workspace_bytes(B, tokens, q.dtype, dims) bytes."""
+    dev, vs, d, args = _packed(q, k, v, beta, gate, offsets)
+    _issue(lib.gdn_chunk,
+           (ctypes.byref(d), *args, *_states(state, state_out, slots, args[0], d, dev),
+            _addr(out, "out", q.dtype, vs, dev), *_scratch(workspace, dev)), dev, stream)
+
+
+def decode(q, k, v, beta, gate, out, state, state_out=None, offsets=None, slots=None,
+           stream=None) -> None:
+    """gdn_decode: the arguments of chunk for sequences of a few tokens;
+    state_out None: in place."""
+    dev, vs, d, args = _packed(q, k, v, beta, gate, offsets)
+    _issue(lib.gdn_decode,
+           (ctypes.byref(d), *args,
+            *_states(state, state if state_out is None else state_out, slots, args[0], d, dev),
+            _addr(out, "out", q.dtype, vs, dev)), dev, stream)

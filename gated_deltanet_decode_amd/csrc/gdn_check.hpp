@@ -1,5 +1,5 @@
 // gdn_check.hpp - argument checks and error reporting shared by the C-ABI
-// sources (gdn_api.cpp, gdn_serve_api.cpp).  All validation happens on the
+// sources (gdn_api.cpp, gdn_serve_api.cpp, gdn_chunk_api.cpp, gdn_f8_api.cpp).  All validation happens on the
 // host before anything is enqueued.
 #pragma once
 
@@ -35,6 +35,22 @@ inline bool overlap(const void *a, size_t na, const void *b, size_t nb) {
     if (!a || !b || na == 0 || nb == 0) return false;
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
     return a0 < b0 + nb && b0 < a0 + na;
+}
+
+// Bytes of an element type, 0 for an unknown code.
+inline size_t type_bytes(int32_t type) {
+    switch (type) {
+    case GDN_F32: return 4;
+    case GDN_BF16:
+    case GDN_F16: return 2;
+    default: return 0;
+    }
+}
+
+inline int check_type(int32_t type, const char *what) {
+    if (type_bytes(type) == 0)
+        return fail(GDN_ERR_SHAPE, "unknown %s %d (GDN_F32, GDN_BF16 or GDN_F16)", what, type);
+    return GDN_OK;
 }
 
 struct Buf {

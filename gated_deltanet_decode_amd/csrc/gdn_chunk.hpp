@@ -1,0 +1,84 @@
+// gdn_chunk.hpp - internal interface between gdn_chunk_api.cpp and the kernels
+// of the delta rule over packed sequences (gdn_chunk.hip, gdn_chunk_back.hip,
+// gdn_decode.hip).  Not installed, not part of the ABI.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "gdn_launch.hpp"
+
+namespace gdn {
+
+constexpr int kChunk = 64;                       // tokens of a chunk
+constexpr int kPlaneBytes = kChunk * kHeadDim * 2;   // one bf16 plane of a chunk's rows
+
+// Packed sequences: sequence b holds tokens offsets[b] .. offsets[b+1] - 1, or
+// tokens / B of them without offsets; its state is at slots[b], or at b.
+struct Packed {
+    const int32_t *offsets;          // [B+1] or NULL
+    const int32_t *slots;            // [B] or NULL
+    int32_t B;
+    int32_t tokens;
+    int32_t n_slots;
+    int32_t Hv;
+    int32_t Hk;
+    int32_t type;                    // of q, k, v, out
+};
+
+// Chunk c of sequence b has place first / 64 + b + c among those of the
+// workspace (first: the sequence's first token): no two chunks share one.
+constexpr int64_t chunk_places(int64_t B, int64_t tokens) { return tokens / kChunk + B; }
+
+// Planes that cut a value of the type exactly, and those of a product whose result
+// is of the type.
+constexpr int planes_in(int type) { return type == 0 ? 3 : type == 1 ? 1 : 2; }
+constexpr int planes_out(int type) { return type == 0 ? 3 : 2; }
+
+// What a chunk's tokens do to each other, per chunk place and value head:
+//   T  (I + A)^-1, its ten lower blocks of 16 x 16 floats, each in the order in
+//      which the lanes of a wave read it as an operand;
+//   P  the masked, decayed and scaled Q K^T in planes_out bf16 planes: six
+//      operands of 16 tokens x 32 tokens each;
+//   vec rise, fall and beta of the 64 tokens;
+// and, unless the inputs are bf16, the planes of k and q per chunk place and key
+// head, as LDS holds them.
+constexpr int kTBlocks = 10, kPBlocks = 6;
+constexpr int kTBytes = kTBlocks * 1024;
+constexpr int kVecFloats = 3 * kChunk;
+constexpr size_t p_bytes(int type) { return static_cast<size_t>(kPBlocks) * 1024 * planes_out(type); }
+
+struct ChunkArgs {
+    Packed s;
+    const void *q;
+    const void *k;
+    const void *v;
+    const float *beta;
+    const float *gate;
+    const float *state;              // NULL: zeros
+    float *state_out;                // NULL: not wanted
+    void *out;
+    // workspace
+    float *T;
+    char *P;
+    float *vec;
+    char *kq;                        // NULL for bf16
+};
+
+struct DecodeArgs {
+    Packed s;
+    const void *q;
+    const void *k;
+    const void *v;
+    const float *beta;
+    const float *gate;
+    const float *state;
+    float *state_out;
+    void *out;
+};
+
+hipError_t launch_chunk(const ChunkArgs &a, hipStream_t s);
+hipError_t launch_decode(const DecodeArgs &a, hipStream_t s);
+
+}  // namespace gdn

@@ -1,0 +1,103 @@
+// gdn_mma.hpp - matrix instructions on float32 values, for the kernels of the
+// delta rule in chunks.  Included by kernel sources only.
+//
+// A product that has to be right to binary32 runs on the bf16 matrix
+// instructions: a float is cut into bf16 pieces ("planes") of 8 significant
+// bits each, every piece exact, and the products of the pieces that matter are
+// summed in the instruction's binary32 accumulators.  bf16 inputs are one
+// plane, fp16 ones two, float32 values three; with planes numbered from 0, the
+// products i + j <= 2 keep an error of about 2^-23 of a term, i + j <= 1 one of
+// 2^-15, which is far below half a step of a 16-bit result.  Three products
+// of one plane with three run at 833 TFLOP/s of the dense bf16 peak, the
+// float32 matrix instructions at 157.
+//
+// Operands of 16 x 16 x 32: lane r + 16 g supplies eight k of row (or column) r
+// and receives rows 4 g..4 g+3 of column r.  Which k a slot (g, e) stands for is
+// free as long as both operands agree, so the two results of 16 rows that a
+// lane holds become an operand of 32 k as they are: slots e < 4 are rows
+// 4 g + e of the first, the others of the second.  Swapping the operands
+// transposes the result.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace gdn {
+namespace {
+
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ f4 mma(u4 a, u4 b, f4 c) {
+    typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, a), __builtin_bit_cast(b8, b), c, 0, 0, 0);
+}
+// 16 x 16 x 16 in binary32: k slot (g, s) is element s of a lane's four.
+__device__ __forceinline__ f4 mma32(f4 a, f4 b, f4 c) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[s], b[s], c, 0, 0, 0);
+    return c;
+}
+
+// The products i + j <= L of an operand of NA planes with one of NB.
+template <int L, int NA, int NB>
+__device__ __forceinline__ f4 mma_planes(const u4 (&a)[NA], const u4 (&b)[NB], f4 c) {
+#pragma unroll
+    for (int t = L; t >= 0; --t)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+                if (i + j == t) c = mma(a[i], b[j], c);
+    return c;
+}
+
+// The upper halves of two words, as two bf16 (truncated floats).
+__device__ __forceinline__ uint32_t upper(uint32_t lo, uint32_t hi) {
+    return __builtin_amdgcn_perm(hi, lo, 0x07060302);
+}
+__device__ __forceinline__ float cut(float x) {            // its first 8 significant bits
+    return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x) & 0xffff0000u);
+}
+
+// The first N planes of eight floats, by truncation: each remainder is exact.
+template <int N>
+__device__ __forceinline__ void planes_of(f4 a, f4 b, u4 (&p)[N]) {
+    float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            p[n][i] = upper(__builtin_bit_cast(uint32_t, x[2 * i]), __builtin_bit_cast(uint32_t, x[2 * i + 1]));
+        if (n + 1 < N)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = x[i] - cut(x[i]);
+    }
+}
+
+// Four 16-bit values of column i (the lane's place among its 16) out of four rows:
+// lane 4 e + c of the sixteen names four consecutive values of row e, columns
+// 4 c..4 c+3.
+__device__ __forceinline__ u2 read_columns(const uint16_t *p) {
+    typedef short s4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s4 *lds4;
+    return __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p)));
+}
+
+// At most N of this wave's vector-memory operations are still on their way, and
+// none of its LDS operations.
+template <int N>
+__device__ __forceinline__ void wait_all() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));
+    asm volatile("" ::: "memory");
+}
+__device__ __forceinline__ void meet() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+}  // namespace
+}  // namespace gdn

@@ -1,0 +1,252 @@
+// gdn_prep.hpp - k_prep, the part of the delta rule in chunks that no state
+// enters: one launch over all chunks, shared by the forward and backward pass.
+// Included by kernel sources only.
+//
+// With g the running sum of the gates in a chunk (g_i - g_j is the log decay
+// from token j to token i), for j <= i < 64:
+//   A_ij = beta_i exp(g_i - g_j) k_i . k_j  (j < i),    T = (I + A)^-1,
+//   P_ij = exp(g_i - g_j) q_i . k_j / sqrt(128).
+// The differences are formed in binary64, so that a token with a strong decay
+// costs the later ones no accuracy.  T is formed by blocks of 16: the diagonal
+// ones by substitution, a column a lane, the others from them by float32
+// matrix products, column of blocks by column.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "gdn_elem.hpp"
+#include "gdn_mma.hpp"
+#include "gdn_packed.hpp"
+
+namespace gdn {
+namespace {
+
+constexpr float kReadScale = 0.08838834764831845f;   // 1 / sqrt(128)
+
+struct PrepArgs {
+    Packed s;
+    const void *q;
+    const void *k;
+    const float *beta;
+    const float *gate;
+    float *T;                        // blocks read along their rows
+    float *Tn;                       // and along their columns; NULL: not wanted
+    char *P;
+    float *vec;
+    char *kq;
+};
+
+// A row of a plane is 16 chunks of 16 bytes; chunk c of row r lies at slot
+// c ^ (r & 15), which spreads the rows that an instruction reads over all banks.
+__device__ __forceinline__ int plane_at(int row, int chunk) { return row * 256 + ((chunk ^ (row & 15)) << 4); }
+
+constexpr int block_of(int it, int jt) { return it * (it + 1) / 2 + jt; }
+// Operand of 16 tokens it x 32 tokens of half h.
+constexpr int pblock_of(int it, int h) { return it < 2 ? it : 2 + (it - 2) * 2 + h; }
+
+// Eight elements from p as planes.
+template <typename ET, int NP>
+__device__ __forceinline__ void load_planes(const void *base, int64_t at, u4 (&p)[NP]) {
+    typedef typename ET::bits bits;
+    const bits *src = static_cast<const bits *>(base) + at;
+    if constexpr (NP == 1) {
+        p[0] = *reinterpret_cast<const u4 *>(src);
+    } else {
+        f4 x, y;
+        const auto v = Pack<bits, 8>::load(src);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = ET::get(v[i]);
+            y[i] = ET::get(v[4 + i]);
+        }
+        planes_of<NP>(x, y, p);
+    }
+}
+
+// The log decay from j to i may pass any number of gates; one of less than -2^14
+// counts as -2^14: no run of gates that float32 can raise again makes up for it
+// (exp of either is 0), and sums stay finite.
+__device__ __forceinline__ double gate_of(float x) { return x < -16384.0f ? -16384.0 : static_cast<double>(x); }
+
+// One workgroup of four waves per chunk place and key head; wave w has the 16
+// tokens w of the chunk as its rows.  The value heads of the key head go through
+// two at a time.
+template <typename ET, int NP, int NO>
+__global__ __launch_bounds__(256) void k_prep(PrepArgs a) {
+    constexpr int HB = 2;
+    __shared__ alignas(16) char kp[NP][kPlaneBytes], qp[NP][kPlaneBytes];
+    __shared__ alignas(16) float As[HB][kTBlocks][256], Td[HB][4][256];
+    __shared__ double gs[HB][kChunk];
+    __shared__ float bs[HB][kChunk];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, g = lane >> 4;
+    const int place = blockIdx.x / a.s.Hk, kh = blockIdx.x - place * a.s.Hk;
+    const int b = sequence_at(a.s, place);
+    const Span sp = span_of(a.s, b);
+    const int c0 = (place - place_of(sp.first, b)) * kChunk;
+    if (c0 < 0 || c0 >= sp.len || slot_of(a.s, b) < 0) return;
+    const int n = min(kChunk, sp.len - c0);            // tokens of this chunk
+    const int64_t t0 = sp.first + c0;
+
+    // rows past the last token are zero
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int at = i * 256 + threadIdx.x, row = at >> 4, chunk = at & 15;
+        u4 pk[NP] = {}, pq[NP] = {};
+        if (row < n) {
+            const int64_t src = ((t0 + row) * a.s.Hk + kh) * kHeadDim + chunk * 8;
+            load_planes<ET, NP>(a.k, src, pk);
+            load_planes<ET, NP>(a.q, src, pq);
+        }
+        const int dst = plane_at(row, chunk);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            *reinterpret_cast<u4 *>(kp[p] + dst) = pk[p];
+            *reinterpret_cast<u4 *>(qp[p] + dst) = pq[p];
+        }
+        if constexpr (NP > 1) {
+            char *to = a.kq + (static_cast<int64_t>(place) * a.s.Hk + kh) * (2 * NP * kPlaneBytes) + dst;
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                *reinterpret_cast<u4 *>(to + p * kPlaneBytes) = pk[p];
+                *reinterpret_cast<u4 *>(to + (NP + p) * kPlaneBytes) = pq[p];
+            }
+        }
+    }
+    __syncthreads();
+    // k_i . k_j and q_i . k_j: lane r has token i = 16 wave + r, elements j = 16 jt + 4 g..
+    f4 kk[4] = {}, qk[4] = {};
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj) {
+        u4 ki[NP], qi[NP];
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const int at = plane_at(wave * 16 + r, 4 * jj + g);
+            ki[p] = *reinterpret_cast<const u4 *>(kp[p] + at);
+            qi[p] = *reinterpret_cast<const u4 *>(qp[p] + at);
+        }
+#pragma unroll
+        for (int jt = 0; jt < 4; ++jt)
+            if (jt <= wave) {
+                u4 kj[NP];
+#pragma unroll
+                for (int p = 0; p < NP; ++p)
+                    kj[p] = *reinterpret_cast<const u4 *>(kp[p] + plane_at(jt * 16 + r, 4 * jj + g));
+                kk[jt] = mma_planes<2>(kj, ki, kk[jt]);
+                qk[jt] = mma_planes<2>(kj, qi, qk[jt]);
+            }
+    }
+    const int group = a.s.Hv / a.s.Hk;
+    for (int h0 = 0; h0 < group; h0 += HB) {
+        if (h0 > 0) __syncthreads();                    // the last heads' columns are done
+        if (wave < HB && h0 + wave < group) {           // running sums of the gates
+            const int h = kh + (h0 + wave) * a.s.Hk;
+            const int64_t at = (t0 + lane) * a.s.Hv + h;
+            const float beta = lane < n ? a.beta[at] : 0.0f;
+            double x = lane < n ? gate_of(a.gate[at]) : 0.0;
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) {
+                const double y = __shfl_up(x, d);
+                if (lane >= d) x += y;
+            }
+            gs[wave][lane] = x;
+            bs[wave][lane] = beta;
+            const double last = lane_of(x, 63);
+            float *vec = a.vec + (static_cast<int64_t>(place) * a.s.Hv + h) * kVecFloats;
+            vec[lane] = expf(static_cast<float>(x));
+            vec[kChunk + lane] = expf(static_cast<float>(last - x));
+            vec[2 * kChunk + lane] = beta;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < HB; ++x) {
+            if (h0 + x >= group) break;
+            const int h = kh + (h0 + x) * a.s.Hk;
+            const int64_t ph = static_cast<int64_t>(place) * a.s.Hv + h;
+            const int i = wave * 16 + r;
+            const double gi = gs[x][i];
+            const float bi = bs[x][i];
+            f4 pv[4] = {};
+#pragma unroll
+            for (int jt = 0; jt < 4; ++jt)
+                if (jt <= wave) {
+                    f4 av;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = jt * 16 + 4 * g + e;
+                        const float d = expf(static_cast<float>(gi - gs[x][j]));
+                        av[e] = j < i ? bi * (d * kk[jt][e]) : 0.0f;
+                        pv[jt][e] = j <= i ? kReadScale * (d * qk[jt][e]) : 0.0f;
+                    }
+                    *reinterpret_cast<f4 *>(&As[x][block_of(wave, jt)][r * 16 + 4 * g]) = av;
+                }
+            char *P = a.P + ph * (kPBlocks * 1024 * NO) + lane * 16;
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                if (half <= wave / 2) {
+                    u4 p[NO];
+                    planes_of<NO>(pv[2 * half], pv[2 * half + 1], p);
+#pragma unroll
+                    for (int m = 0; m < NO; ++m)
+                        *reinterpret_cast<u4 *>(P + (m * kPBlocks + pblock_of(wave, half)) * 1024) = p[m];
+                }
+        }
+        __syncthreads();
+        if (wave < HB && h0 + wave < group) {           // column r of diagonal block g
+            const float *A = As[wave][block_of(g, g)];
+            float x[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float s = i == r ? 1.0f : 0.0f;
+#pragma unroll
+                for (int j = 0; j < i; ++j) s = fmaf(-A[i * 16 + j], x[j], s);
+                x[i] = s;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) Td[wave][g][i * 16 + r] = x[i];
+        }
+        __syncthreads();
+        // Columns of blocks: wave 0 and 1 have the first of a head each, 2 and 3 the
+        // other three.
+        const int x = wave % HB;
+        if (h0 + x < group) {
+            const int h = kh + (h0 + x) * a.s.Hk;
+            const int64_t ph = static_cast<int64_t>(place) * a.s.Hv + h;
+            float *T = a.T + ph * (kTBlocks * 256) + lane * 4;
+            float *Tn = a.Tn ? a.Tn + ph * (kTBlocks * 256) + lane * 4 : nullptr;
+            const int j0 = wave < HB ? 0 : 1, j1 = wave < HB ? 1 : 4;
+            for (int j = j0; j < j1; ++j) {
+                f4 col[4];                              // T_ij, lane r column r, rows 4 g..
+#pragma unroll
+                for (int e = 0; e < 4; ++e) col[0][e] = Td[x][j][(4 * g + e) * 16 + r];
+                *reinterpret_cast<f4 *>(T + block_of(j, j) * 256) =
+                    *reinterpret_cast<const f4 *>(&Td[x][j][r * 16 + 4 * g]);
+                if (Tn) *reinterpret_cast<f4 *>(Tn + block_of(j, j) * 256) = col[0];
+#pragma unroll
+                for (int d = 1; d < 4; ++d) {
+                    const int i = j + d;
+                    if (i > 3) break;
+                    f4 s = {0, 0, 0, 0};
+#pragma unroll
+                    for (int m = 0; m < d; ++m)
+                        s = mma32(*reinterpret_cast<const f4 *>(&As[x][block_of(i, j + m)][r * 16 + 4 * g]), col[m], s);
+                    s = -s;
+                    const f4 diag = *reinterpret_cast<const f4 *>(&Td[x][i][r * 16 + 4 * g]);
+                    col[d] = mma32(diag, s, f4{0, 0, 0, 0});
+                    *reinterpret_cast<f4 *>(T + block_of(i, j) * 256) = mma32(s, diag, f4{0, 0, 0, 0});
+                    if (Tn) *reinterpret_cast<f4 *>(Tn + block_of(i, j) * 256) = col[d];
+                }
+            }
+        }
+    }
+}
+
+template <typename ET, int NP, int NO>
+hipError_t launch_prep_of(const PrepArgs &a, hipStream_t s) {
+    const int64_t wgs = chunk_places(a.s.B, a.s.tokens) * a.s.Hk;
+    k_prep<ET, NP, NO><<<dim3(static_cast<unsigned>(wgs)), dim3(256), 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace gdn

@@ -17,25 +17,11 @@ namespace {
 using gdn::Buf;
 using gdn::check_alias;
 using gdn::check_ptrs;
+using gdn::check_type;
 using gdn::clear_error;
 using gdn::fail;
 using gdn::hip_status;
-
-// Bytes of an element type, 0 for an unknown code.
-size_t type_bytes(int32_t type) {
-    switch (type) {
-    case GDN_F32: return 4;
-    case GDN_BF16:
-    case GDN_F16: return 2;
-    default: return 0;
-    }
-}
-
-int check_type(int32_t type, const char *what) {
-    if (type_bytes(type) == 0)
-        return fail(GDN_ERR_SHAPE, "unknown %s %d (GDN_F32, GDN_BF16 or GDN_F16)", what, type);
-    return GDN_OK;
-}
+using gdn::type_bytes;
 
 int check_rows(int32_t rows, int32_t n) {
     const int64_t most = UINT32_MAX / gdn::kQuantMaxThreads;   // one workgroup per row

@@ -58,7 +58,7 @@
 extern "C" {
 #endif
 
-#define GDN_VERSION 10400 /* 1.4.0 */
+#define GDN_VERSION 10500 /* 1.5.0 */
 
 #define GDN_OK 0
 #define GDN_ERR_NULL (-1)      /* a required pointer is NULL                  */
@@ -491,6 +491,67 @@ size_t gdn_verify_workspace_bytes(int32_t B, int32_t V);
 int gdn_pair_commit(const gdn_dims *dims, int32_t layers, int32_t B, const int32_t *accepted,
                     float *state, const float *state_next, int32_t conv_floats, float *conv_state,
                     const float *conv_state_next, void *stream);
+
+/*
+ * The delta rule over packed sequences: prompts and training sequences in chunks
+ * on the matrix cores (gdn_chunk), and decoded tokens one by one
+ * (gdn_decode).  Both compute the recurrence of gdn_step for every sequence, with
+ * q, k, v and out in float32, bfloat16 or float16 (`type`, all of one type) and
+ * beta, gate and the states in float32.
+ *   q, k     [tokens][n_k_heads][d_k]    the sequences' tokens one after another
+ *   v, out   [tokens][n_v_heads][d_v]
+ *   beta, gate [tokens][n_v_heads]
+ *   offsets  [B+1] int32, optional: sequence b holds the tokens offsets[b] up
+ *            to, not including, offsets[b+1] (none: its state is handed on).
+ *            NULL: B sequences of tokens / B.  Rows that belong to no sequence
+ *            are neither read nor written.  Offsets must not descend; ones
+ *            outside [0, tokens] count as the nearer end, and one below the one
+ *            before it as equal to it (tokens that two sequences then share hold
+ *            either's output).
+ *   slots    [B] int32, optional: the states of sequence b are those at slots[b];
+ *            a sequence whose slot is outside [0, n_slots) is left out, and
+ *            none of its rows is written (a padded batch).  Two sequences with
+ *            one slot leave the state of either.  NULL: slot b, n_slots = B.
+ *   state    [n_slots][n_v_heads][d_v][d_k]  before each sequence's first token
+ *   state_out  the same shape: after its last; may be `state` itself (in
+ *            place).  Slots that no sequence names are not written.
+ * Alignment: q, k, v, out, the states and the workspace 16 bytes, the others 4.
+ * Limits (GDN_ERR_SHAPE beyond): B, tokens >= 1, n_v_heads <= 65535, B *
+ * n_v_heads <= 8388607 (gdn_decode: 4194303), and for gdn_chunk (tokens / 64 +
+ * B) * n_v_heads <= 8388607.
+ *
+ * gdn_chunk takes 64 tokens at a time: the corrections of a chunk's tokens are
+ * the solution of a triangular system, and everything else is matrix products.
+ * The state, the corrections and all sums are float32, and products whose result
+ * enters the state or a float32 output are right to about 2^-23 of their terms;
+ * outputs of 16 bits are rounded once, from sums right to 2^-15.  Results
+ * depend neither on B nor on the other sequences.  A NaN or an infinity in a
+ * token reaches the state from its chunk on and may reach all outputs of its
+ * chunk, those of the chunk's earlier tokens too.
+ *   state      NULL: zeros
+ *   state_out  NULL: not wanted
+ *   workspace  gdn_chunk_workspace_bytes(dims, B, tokens, type) bytes.  Two calls
+ *              that may overlap in time need a workspace each.
+ */
+int gdn_chunk(const gdn_dims *dims, int32_t B, int32_t tokens, int32_t type, const void *q,
+              const void *k, const void *v, const float *beta, const float *gate,
+              const int32_t *offsets, const int32_t *slots, int32_t n_slots, const float *state,
+              float *state_out, void *out, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace gdn_chunk needs (0 on invalid arguments). */
+size_t gdn_chunk_workspace_bytes(const gdn_dims *dims, int32_t B, int32_t tokens, int32_t type);
+
+/*
+ * gdn_decode - the same for sequences of one or a few tokens (any number is
+ * right, but their time grows with the longest): each state is read once and
+ * written once.  The arithmetic is gdn_step's on the inputs as float32: for
+ * float32 the bits are those of gdn_step, token by token.  `state` and
+ * `state_out` are required.
+ */
+int gdn_decode(const gdn_dims *dims, int32_t B, int32_t tokens, int32_t type, const void *q,
+               const void *k, const void *v, const float *beta, const float *gate,
+               const int32_t *offsets, const int32_t *slots, int32_t n_slots, const float *state,
+               float *state_out, void *out, void *stream);
 
 /* Message for the last non-zero return on this thread ("" if none). */
 const char *gdn_last_error(void);
