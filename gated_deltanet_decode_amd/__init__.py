@@ -32,6 +32,10 @@ C entry points:
     chunk(q, k, v, beta, gate, out, state, state_out, offsets, slots, workspace)
                                                  -> gdn_chunk
     chunk_workspace_bytes(B, tokens, dtype)      -> gdn_chunk_workspace_bytes
+    chunk_backward(q, k, v, beta, gate, d_out, dq, dk, dv, dbeta, dgate, ...)
+                                                 -> gdn_chunk_backward
+    chunk_backward_workspace_bytes(B, tokens, dtype)
+                                                 -> gdn_chunk_backward_workspace_bytes
     decode(q, k, v, beta, gate, out, state, state_out, offsets, slots) -> gdn_decode
     last_error(), version()
 
@@ -52,7 +56,7 @@ __all__ = ["GdnError", "Dims", "TailParams", "GateInputs", "lib", "step", "bind_
            "layer_tail_ba",
            "layer_tail_ba_workspace_bytes", "add_rmsnorm_q8", "quantize_q8", "linear_q8",
            "verify", "verify_workspace_bytes", "pair_commit", "chunk", "chunk_workspace_bytes",
-           "decode", "last_error", "version", "PAGE_DIMS",
+           "chunk_backward", "chunk_backward_workspace_bytes", "decode", "last_error", "version", "PAGE_DIMS",
            "PAGE_TAIL", "ERRORS"]
 
 if not os.path.exists(LIBRARY):
@@ -153,6 +157,10 @@ lib.gdn_chunk.argtypes = [_DP] + [_i32] * 3 + [_vp] * 7 + [_i32] + [_vp] * 3 + \
     [_vp, ctypes.c_size_t, _vp]
 lib.gdn_chunk_workspace_bytes.restype = ctypes.c_size_t
 lib.gdn_chunk_workspace_bytes.argtypes = [_DP] + [_i32] * 3
+lib.gdn_chunk_backward.restype = ctypes.c_int
+lib.gdn_chunk_backward.argtypes = [_DP] + [_i32] * 3 + [_vp] * 15 + [_vp, ctypes.c_size_t, _vp]
+lib.gdn_chunk_backward_workspace_bytes.restype = ctypes.c_size_t
+lib.gdn_chunk_backward_workspace_bytes.argtypes = [_DP] + [_i32] * 3
 lib.gdn_decode.restype = ctypes.c_int
 lib.gdn_decode.argtypes = [_DP] + [_i32] * 3 + [_vp] * 7 + [_i32] + [_vp] * 3 + [_vp]
 
@@ -683,10 +691,18 @@ def _scratch(workspace, dev):
     return ptr, size
 
 
-def chunk_workspace_bytes(B: int, tokens: int, dtype, dims: Dims = PAGE_DIMS) -> int:
+def _chunk_bytes(fn, B, tokens, dtype, dims):
     if dtype not in _TYPES or not (0 < B <= _INT32_MAX and 0 < tokens <= _INT32_MAX):
         return 0
-    return int(lib.gdn_chunk_workspace_bytes(ctypes.byref(dims), B, tokens, _TYPES[dtype]))
+    return int(fn(ctypes.byref(dims), B, tokens, _TYPES[dtype]))
+
+
+def chunk_workspace_bytes(B: int, tokens: int, dtype, dims: Dims = PAGE_DIMS) -> int:
+    return _chunk_bytes(lib.gdn_chunk_workspace_bytes, B, tokens, dtype, dims)
+
+
+def chunk_backward_workspace_bytes(B: int, tokens: int, dtype, dims: Dims = PAGE_DIMS) -> int:
+    return _chunk_bytes(lib.gdn_chunk_backward_workspace_bytes, B, tokens, dtype, dims)
 
 
 def chunk(q, k, v, beta, gate, out, state=None, state_out=None, offsets=None, slots=None,
@@ -701,6 +717,29 @@ def chunk(q, k, v, beta, gate, out, state=None, state_out=None, offsets=None, sl
     _issue(lib.gdn_chunk,
            (ctypes.byref(d), *args, *_states(state, state_out, slots, args[0], d, dev),
             _addr(out, "out", q.dtype, vs, dev), *_scratch(workspace, dev)), dev, stream)
+
+
+def chunk_backward(q, k, v, beta, gate, d_out, dq, dk, dv, dbeta, dgate, state=None,
+                   d_state_out=None, d_state=None, offsets=None, workspace=None,
+                   stream=None) -> None:
+    """gdn_chunk_backward: q, k, v, beta, gate, offsets and state as given to chunk
+    (no slots), d_out like its out; dq, dk, dv, dbeta and dgate like the inputs.
+    d_state_out (None: zeros) and d_state (None: not wanted; may be d_state_out)
+    [B][Hv][dv][dk] float32.  workspace: a GPU tensor of at least
+    chunk_backward_workspace_bytes(B, tokens, q.dtype, dims) bytes."""
+    dev, vs, d, args = _packed(q, k, v, beta, gate, offsets)
+    t, ks, bs = q.dtype, tuple(q.shape), vs[:-1]
+    st = (args[0], d.n_v_heads, d.d_v, d.d_k)
+
+    def opt(x, name):
+        return None if x is None else _addr(x, name, _F32, st, dev)
+
+    _issue(lib.gdn_chunk_backward,
+           (ctypes.byref(d), *args, opt(state, "state"), _addr(d_out, "d_out", t, vs, dev),
+            opt(d_state_out, "d_state_out"), _addr(dq, "dq", t, ks, dev), _addr(dk, "dk", t, ks, dev),
+            _addr(dv, "dv", t, vs, dev), _addr(dbeta, "dbeta", _F32, bs, dev),
+            _addr(dgate, "dgate", _F32, bs, dev), opt(d_state, "d_state"),
+            *_scratch(workspace, dev)), dev, stream)
 
 
 def decode(q, k, v, beta, gate, out, state, state_out=None, offsets=None, slots=None,

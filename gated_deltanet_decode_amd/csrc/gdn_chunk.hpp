@@ -64,6 +64,31 @@ struct ChunkArgs {
     char *P;
     float *vec;
     char *kq;                        // NULL for bf16
+    // the backward pass alone
+    const void *d_out;
+    float *states;                   // [place][Hv][dv][dk] that enter the chunks
+    float *delta;                    // [place][Hv][64][dv]
+    float *od;                       // [place][Hv][8][64] sums of out * d_out over 16 rows each
+};
+
+// The backward pass.  After k_prep and k_walk, k_back goes along the sequences in
+// reverse with the state's gradient, and k_grad forms what remains per chunk.
+struct BackArgs {
+    ChunkArgs f;
+    const float *d_state_out;        // NULL: zeros
+    float *d_state;                  // NULL: not wanted
+    void *dq;
+    void *dk;
+    void *dv;
+    float *dbeta;
+    float *dgate;
+    // workspace
+    float *Tn;                       // T's blocks, read along their columns
+    char *Pn;                        // P's operands transposed, three planes
+    double *gsum;                    // [place][Hv][64] running sums of the gates
+    float *dstates;                  // [place][Hv][dv][dk] that leave the chunks
+    float *r;                        // [place][Hv][64][dv]
+    float *du;                       // [place][Hv][8] sums of delta * (gradient of M' k) over 16 rows
 };
 
 struct DecodeArgs {
@@ -79,6 +104,7 @@ struct DecodeArgs {
 };
 
 hipError_t launch_chunk(const ChunkArgs &a, hipStream_t s);
+hipError_t launch_chunk_backward(const BackArgs &a, hipStream_t s);
 hipError_t launch_decode(const DecodeArgs &a, hipStream_t s);
 
 }  // namespace gdn

@@ -84,6 +84,31 @@ struct ChunkSpace {
     }
 };
 
+struct BackSpace {
+    size_t T, P, vec, kq, Tn, Pn, gsum, states, dstates, delta, r, od, du, bytes;
+    BackSpace(const gdn_dims *d, int32_t B, int32_t tokens, int32_t type) {
+        const size_t places = static_cast<size_t>(gdn::chunk_places(B, tokens));
+        const size_t pv = places * d->n_v_heads, pk = places * d->n_k_heads;
+        const size_t f = sizeof(float), D = gdn::kHeadDim, C = gdn::kChunk;
+        size_t at = 0;
+        const auto take = [&](size_t n) { const size_t x = at; at += n; return x; };
+        gsum = take(pv * C * sizeof(double));
+        states = take(pv * D * D * f);
+        dstates = take(pv * D * D * f);
+        delta = take(pv * C * D * f);
+        r = take(pv * C * D * f);
+        T = take(pv * gdn::kTBytes);
+        Tn = take(pv * gdn::kTBytes);
+        P = take(pv * gdn::p_bytes(GDN_F32));
+        Pn = take(pv * gdn::p_bytes(GDN_F32));
+        vec = take(pv * gdn::kVecFloats * f);
+        od = take(pv * 8 * C * f);
+        du = take(pv * 8 * f);
+        kq = take(type == GDN_BF16 ? 0 : pk * 2 * gdn::planes_in(type) * gdn::kPlaneBytes);
+        bytes = at;
+    }
+};
+
 gdn::Packed packed(const gdn_dims *d, int32_t B, int32_t tokens, int32_t type, const int32_t *offsets,
                    const int32_t *slots, int32_t n_slots) {
     gdn::Packed s{};
@@ -165,6 +190,80 @@ int gdn_chunk(const gdn_dims *dims, int32_t B, int32_t tokens, int32_t type, con
     a.kq = type == GDN_BF16 ? nullptr : p + w.kq;
     (void)hipGetLastError();
     return hip_status(gdn::launch_chunk(a, static_cast<hipStream_t>(stream)), "gdn_chunk launch");
+}
+
+size_t gdn_chunk_backward_workspace_bytes(const gdn_dims *dims, int32_t B, int32_t tokens, int32_t type) {
+    return sizes_ok(dims, B, tokens, type) ? BackSpace(dims, B, tokens, type).bytes : 0;
+}
+
+int gdn_chunk_backward(const gdn_dims *dims, int32_t B, int32_t tokens, int32_t type, const void *q,
+                       const void *k, const void *v, const float *beta, const float *gate,
+                       const int32_t *offsets, const float *state, const void *d_out,
+                       const float *d_state_out, void *dq, void *dk, void *dv, float *dbeta, float *dgate,
+                       float *d_state, void *workspace, size_t workspace_bytes, void *stream) {
+    clear_error();
+    GDN_TRY(check_packed(dims, B, tokens, type, offsets));
+    GDN_TRY(check_places(dims, B, tokens));
+    const BackSpace w(dims, B, tokens, type);
+    GDN_TRY(check_workspace(workspace, workspace_bytes, w.bytes));
+    const size_t z = type_bytes(type), n = static_cast<size_t>(tokens), D = gdn::kHeadDim;
+    const size_t nk = n * dims->n_k_heads * D * z, nv = n * dims->n_v_heads * D * z;
+    const size_t ns = static_cast<size_t>(B) * dims->n_v_heads * D * D * sizeof(float);
+    const size_t nb = n * dims->n_v_heads * sizeof(float);
+    Buf vec[10] = {{"dq", dq, nk}, {"dk", dk, nk}, {"dv", dv, nv}, {"q", q, nk}, {"k", k, nk}, {"v", v, nv},
+                   {"d_out", d_out, nv}};
+    int n_vec = 7;
+    if (state) vec[n_vec++] = {"state", state, ns};
+    // in place is one buffer under two names
+    if (d_state_out && d_state_out != d_state) vec[n_vec++] = {"d_state_out", d_state_out, ns};
+    if (d_state) vec[n_vec++] = {"d_state", d_state, ns};
+    const Buf sc[] = {{"dbeta", dbeta, nb}, {"dgate", dgate, nb}, {"beta", beta, nb}, {"gate", gate, nb},
+                      {"offsets", offsets, (static_cast<size_t>(B) + 1) * sizeof(int32_t)}};
+    const int n_sc = offsets ? 5 : 4;
+    GDN_TRY(check_ptrs(vec, n_vec, 16));
+    GDN_TRY(check_ptrs(sc, n_sc, 4));
+    Buf all[16], outs[7] = {vec[0], vec[1], vec[2], sc[0], sc[1]};
+    int n_all = 0, n_out = 5;
+    for (int i = 0; i < n_vec; ++i) all[n_all++] = vec[i];
+    for (int i = 0; i < n_sc; ++i) all[n_all++] = sc[i];
+    all[n_all++] = outs[n_out++] = {"workspace", workspace, w.bytes};
+    if (d_state) outs[n_out++] = vec[n_vec - 1];
+    GDN_TRY(check_alias(outs, n_out, all, n_all));
+
+    char *p = static_cast<char *>(workspace);
+    const auto at = [&](size_t x) { return reinterpret_cast<float *>(p + x); };
+    gdn::BackArgs a{};
+    a.f.s = packed(dims, B, tokens, type, offsets, nullptr, B);
+    a.f.q = q;
+    a.f.k = k;
+    a.f.v = v;
+    a.f.beta = beta;
+    a.f.gate = gate;
+    a.f.state = state;
+    a.f.d_out = d_out;
+    a.f.T = at(w.T);
+    a.f.P = p + w.P;
+    a.f.vec = at(w.vec);
+    a.f.kq = type == GDN_BF16 ? nullptr : p + w.kq;
+    a.f.states = at(w.states);
+    a.f.delta = at(w.delta);
+    a.f.od = at(w.od);
+    a.d_state_out = d_state_out;
+    a.d_state = d_state;
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    a.dbeta = dbeta;
+    a.dgate = dgate;
+    a.Tn = at(w.Tn);
+    a.Pn = p + w.Pn;
+    a.gsum = reinterpret_cast<double *>(p + w.gsum);
+    a.dstates = at(w.dstates);
+    a.r = at(w.r);
+    a.du = at(w.du);
+    (void)hipGetLastError();
+    return hip_status(gdn::launch_chunk_backward(a, static_cast<hipStream_t>(stream)),
+                      "gdn_chunk_backward launch");
 }
 
 int gdn_decode(const gdn_dims *dims, int32_t B, int32_t tokens, int32_t type, const void *q, const void *k,

@@ -79,7 +79,7 @@ __device__ __forceinline__ void planes_of(f4 a, f4 b, u4 (&p)[N]) {
 // Four 16-bit values of column i (the lane's place among its 16) out of four rows:
 // lane 4 e + c of the sixteen names four consecutive values of row e, columns
 // 4 c..4 c+3.
-__device__ __forceinline__ u2 read_columns(const uint16_t *p) {
+__device__ __forceinline__ u2 read_columns(const char *p) {
     typedef short s4 __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) s4 *lds4;
     return __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p)));

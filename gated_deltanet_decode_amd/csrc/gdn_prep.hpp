@@ -30,10 +30,13 @@ struct PrepArgs {
     const float *beta;
     const float *gate;
     float *T;                        // blocks read along their rows
-    float *Tn;                       // and along their columns; NULL: not wanted
     char *P;
     float *vec;
     char *kq;
+    // the backward pass alone
+    float *Tn;                       // and along their columns
+    char *Pn;
+    double *gsum;
 };
 
 // A row of a plane is 16 chunks of 16 bytes; chunk c of row r lies at slot
@@ -43,6 +46,9 @@ __device__ __forceinline__ int plane_at(int row, int chunk) { return row * 256 +
 constexpr int block_of(int it, int jt) { return it * (it + 1) / 2 + jt; }
 // Operand of 16 tokens it x 32 tokens of half h.
 constexpr int pblock_of(int it, int h) { return it < 2 ? it : 2 + (it - 2) * 2 + h; }
+
+// Transposed: operand of 16 tokens jt x the 32 tokens of half h, h >= jt / 2.
+constexpr int pnblock_of(int jt, int h) { return jt < 2 ? jt * 2 + h : 4 + (jt - 2); }
 
 // Eight elements from p as planes.
 template <typename ET, int NP>
@@ -68,10 +74,18 @@ __device__ __forceinline__ void load_planes(const void *base, int64_t at, u4 (&p
 // (exp of either is 0), and sums stay finite.
 __device__ __forceinline__ double gate_of(float x) { return x < -16384.0f ? -16384.0 : static_cast<double>(x); }
 
+// The backward pass divides corrections by beta; one of (nearly) 0 counts there as
+// 2^-60, whose corrections are below any rounding.
+constexpr float kLeastBeta = 0x1p-60f;
+template <bool kBack>
+__device__ __forceinline__ float beta_of(float x) {
+    return kBack && fabsf(x) < kLeastBeta ? kLeastBeta : x;
+}
+
 // One workgroup of four waves per chunk place and key head; wave w has the 16
 // tokens w of the chunk as its rows.  The value heads of the key head go through
 // two at a time.
-template <typename ET, int NP, int NO>
+template <typename ET, int NP, int NO, bool kBack>
 __global__ __launch_bounds__(256) void k_prep(PrepArgs a) {
     constexpr int HB = 2;
     __shared__ alignas(16) char kp[NP][kPlaneBytes], qp[NP][kPlaneBytes];
@@ -115,7 +129,7 @@ __global__ __launch_bounds__(256) void k_prep(PrepArgs a) {
     }
     __syncthreads();
     // k_i . k_j and q_i . k_j: lane r has token i = 16 wave + r, elements j = 16 jt + 4 g..
-    f4 kk[4] = {}, qk[4] = {};
+    f4 kk[4] = {}, qk[4] = {}, kq[4] = {};                // kq: lane r token j, elements i
 #pragma unroll
     for (int jj = 0; jj < 4; ++jj) {
         u4 ki[NP], qi[NP];
@@ -134,6 +148,7 @@ __global__ __launch_bounds__(256) void k_prep(PrepArgs a) {
                     kj[p] = *reinterpret_cast<const u4 *>(kp[p] + plane_at(jt * 16 + r, 4 * jj + g));
                 kk[jt] = mma_planes<2>(kj, ki, kk[jt]);
                 qk[jt] = mma_planes<2>(kj, qi, qk[jt]);
+                if constexpr (kBack) kq[jt] = mma_planes<2>(qi, kj, kq[jt]);
             }
     }
     const int group = a.s.Hv / a.s.Hk;
@@ -142,7 +157,7 @@ __global__ __launch_bounds__(256) void k_prep(PrepArgs a) {
         if (wave < HB && h0 + wave < group) {           // running sums of the gates
             const int h = kh + (h0 + wave) * a.s.Hk;
             const int64_t at = (t0 + lane) * a.s.Hv + h;
-            const float beta = lane < n ? a.beta[at] : 0.0f;
+            const float beta = lane < n ? beta_of<kBack>(a.beta[at]) : 0.0f;
             double x = lane < n ? gate_of(a.gate[at]) : 0.0;
 #pragma unroll
             for (int d = 1; d < 64; d *= 2) {
@@ -156,6 +171,7 @@ __global__ __launch_bounds__(256) void k_prep(PrepArgs a) {
             vec[lane] = expf(static_cast<float>(x));
             vec[kChunk + lane] = expf(static_cast<float>(last - x));
             vec[2 * kChunk + lane] = beta;
+            if constexpr (kBack) a.gsum[(static_cast<int64_t>(place) * a.s.Hv + h) * kChunk + lane] = x;
         }
         __syncthreads();
 #pragma unroll
@@ -190,6 +206,32 @@ __global__ __launch_bounds__(256) void k_prep(PrepArgs a) {
                     for (int m = 0; m < NO; ++m)
                         *reinterpret_cast<u4 *>(P + (m * kPBlocks + pblock_of(wave, half)) * 1024) = p[m];
                 }
+            if constexpr (kBack) {
+                // operand (jt, half): lane r token j, eight tokens i of the tiles 2 half
+                // and 2 half + 1; this wave's four of them.  Operands whose tiles lie
+                // all above the diagonal do not exist.
+                char *Pn = a.Pn + ph * (kPBlocks * 1024 * 3) + lane * 16 + 8 * (wave & 1);
+#pragma unroll
+                for (int jt = 0; jt < 4; ++jt) {
+                    if (jt / 2 > wave / 2) continue;
+                    f4 pv = {0, 0, 0, 0};
+                    if (jt <= wave) {
+                        const int j = jt * 16 + r;
+                        const double gj = gs[x][j];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int i = wave * 16 + 4 * g + e;
+                            const float d = expf(static_cast<float>(gs[x][i] - gj));
+                            pv[e] = j <= i ? kReadScale * (d * kq[jt][e]) : 0.0f;
+                        }
+                    }
+                    u4 p[3];
+                    planes_of<3>(pv, pv, p);
+#pragma unroll
+                    for (int m = 0; m < 3; ++m)
+                        *reinterpret_cast<u2 *>(Pn + (m * kPBlocks + pnblock_of(jt, wave / 2)) * 1024) = u2{p[m].x, p[m].y};
+                }
+            }
         }
         __syncthreads();
         if (wave < HB && h0 + wave < group) {           // column r of diagonal block g
@@ -213,7 +255,7 @@ __global__ __launch_bounds__(256) void k_prep(PrepArgs a) {
             const int h = kh + (h0 + x) * a.s.Hk;
             const int64_t ph = static_cast<int64_t>(place) * a.s.Hv + h;
             float *T = a.T + ph * (kTBlocks * 256) + lane * 4;
-            float *Tn = a.Tn ? a.Tn + ph * (kTBlocks * 256) + lane * 4 : nullptr;
+            float *Tn = kBack ? a.Tn + ph * (kTBlocks * 256) + lane * 4 : nullptr;
             const int j0 = wave < HB ? 0 : 1, j1 = wave < HB ? 1 : 4;
             for (int j = j0; j < j1; ++j) {
                 f4 col[4];                              // T_ij, lane r column r, rows 4 g..
@@ -221,7 +263,7 @@ __global__ __launch_bounds__(256) void k_prep(PrepArgs a) {
                 for (int e = 0; e < 4; ++e) col[0][e] = Td[x][j][(4 * g + e) * 16 + r];
                 *reinterpret_cast<f4 *>(T + block_of(j, j) * 256) =
                     *reinterpret_cast<const f4 *>(&Td[x][j][r * 16 + 4 * g]);
-                if (Tn) *reinterpret_cast<f4 *>(Tn + block_of(j, j) * 256) = col[0];
+                if constexpr (kBack) *reinterpret_cast<f4 *>(Tn + block_of(j, j) * 256) = col[0];
 #pragma unroll
                 for (int d = 1; d < 4; ++d) {
                     const int i = j + d;
@@ -234,17 +276,17 @@ __global__ __launch_bounds__(256) void k_prep(PrepArgs a) {
                     const f4 diag = *reinterpret_cast<const f4 *>(&Td[x][i][r * 16 + 4 * g]);
                     col[d] = mma32(diag, s, f4{0, 0, 0, 0});
                     *reinterpret_cast<f4 *>(T + block_of(i, j) * 256) = mma32(s, diag, f4{0, 0, 0, 0});
-                    if (Tn) *reinterpret_cast<f4 *>(Tn + block_of(i, j) * 256) = col[d];
+                    if constexpr (kBack) *reinterpret_cast<f4 *>(Tn + block_of(i, j) * 256) = col[d];
                 }
             }
         }
     }
 }
 
-template <typename ET, int NP, int NO>
-hipError_t launch_prep_of(const PrepArgs &a, hipStream_t s) {
+template <typename ET, int NP, int NO, bool kBack>
+hipError_t launch_prep(const PrepArgs &a, hipStream_t s) {
     const int64_t wgs = chunk_places(a.s.B, a.s.tokens) * a.s.Hk;
-    k_prep<ET, NP, NO><<<dim3(static_cast<unsigned>(wgs)), dim3(256), 0, s>>>(a);
+    k_prep<ET, NP, NO, kBack><<<dim3(static_cast<unsigned>(wgs)), dim3(256), 0, s>>>(a);
     return hipGetLastError();
 }
 

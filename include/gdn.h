@@ -542,6 +542,40 @@ int gdn_chunk(const gdn_dims *dims, int32_t B, int32_t tokens, int32_t type, con
 size_t gdn_chunk_workspace_bytes(const gdn_dims *dims, int32_t B, int32_t tokens, int32_t type);
 
 /*
+ * gdn_chunk_backward - the gradients of gdn_chunk, for a loss whose gradients of
+ * out and state_out are d_out and d_state_out:
+ *   d_out, dv  [tokens][n_v_heads][d_v]    of `type`
+ *   dq, dk     [tokens][n_k_heads][d_k]    of `type`: sums over the value heads
+ *              that share the key head, formed in float32 and rounded once
+ *   dbeta, dgate [tokens][n_v_heads]       float32
+ *   state      [B][n_v_heads][d_v][d_k]    as given to gdn_chunk; NULL: zeros
+ *   d_state_out  the same shape; NULL: zeros
+ *   d_state    the same shape, optional: the gradient of `state`; may be
+ *              d_state_out itself
+ * Sequence b's state is the b-th (no slots).  The forward pass is run again
+ * inside: nothing of it needs to be kept but its inputs.  Every state, correction
+ * and sum is float32, and so is all that dbeta, dgate, d_state and float32
+ * gradients are made of (right to about 2^-23 of the terms); 16-bit dq and dk are
+ * rounded once, from sums right to 2^-15.  A beta of magnitude below 2^-60 counts as
+ * 2^-60 in the corrections and as 0 in dv, which changes no gradient by a float32
+ * rounding.  A sum of gates that falls by more than 2^14 in one token is held
+ * there (its exp is 0 either way).  Rows of no sequence are not written.
+ *   workspace  gdn_chunk_backward_workspace_bytes(dims, B, tokens, type) bytes:
+ *              the states that enter and the gradients that leave every chunk
+ *              (260 KB a chunk of 64 tokens and value head)
+ */
+int gdn_chunk_backward(const gdn_dims *dims, int32_t B, int32_t tokens, int32_t type, const void *q,
+                       const void *k, const void *v, const float *beta, const float *gate,
+                       const int32_t *offsets, const float *state, const void *d_out,
+                       const float *d_state_out, void *dq, void *dk, void *dv, float *dbeta,
+                       float *dgate, float *d_state, void *workspace, size_t workspace_bytes,
+                       void *stream);
+
+/* Bytes of workspace gdn_chunk_backward needs (0 on invalid arguments). */
+size_t gdn_chunk_backward_workspace_bytes(const gdn_dims *dims, int32_t B, int32_t tokens,
+                                          int32_t type);
+
+/*
  * gdn_decode - the same for sequences of one or a few tokens (any number is
  * right, but their time grows with the longest): each state is read once and
  * written once.  The arithmetic is gdn_step's on the inputs as float32: for

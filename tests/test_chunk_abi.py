@@ -98,3 +98,49 @@ def test_binding_refusals(g):
         g.decode(q.int(), q, v, b, b, v, None)
     with pytest.raises(ValueError, match="required"):
         g.decode(None, q, v, b, b, v, None)
+
+
+BACK = ("q", "k", "v", "beta", "gate", "offsets", "state", "d_out", "d_state_out", "dq", "dk", "dv", "dbeta", "dgate",
+        "d_state")
+
+
+def test_backward_refusals(g):
+    base = {n: BASE + i * STEP for i, n in enumerate(BACK + ("ws",))}
+
+    def f(hv=4, hk=2, dk_=128, B=3, tokens=100, type=1, bytes=None, **over):
+        a = dict(base, **over)
+        d = g.Dims(hv, hk, dk_, 128)
+        if bytes is None:
+            bytes = g.lib.gdn_chunk_backward_workspace_bytes(ctypes.byref(d), B, tokens, type)
+        return g.lib.gdn_chunk_backward(ctypes.byref(d), B, tokens, type, *(a[n] for n in BACK), a["ws"], bytes, None)
+
+    for n in BACK:
+        if n not in ("offsets", "state", "d_state_out", "d_state"):
+            expect(g, f(**{n: None}), -1, n)
+    expect(g, f(hv=3), -2, "multiple")
+    expect(g, f(dk_=64), -2, "d_k")
+    expect(g, f(B=0), -2, "B must")
+    expect(g, f(tokens=0), -2, "tokens must")
+    expect(g, f(type=5), -2, "type")
+    expect(g, f(offsets=None), -2, "multiple of B")
+    expect(g, f(hv=1024, hk=1, tokens=1 << 20, bytes=1 << 60), -2, "64")
+    for n in ("q", "k", "v", "state", "d_out", "d_state_out", "dq", "dk", "dv", "d_state"):
+        expect(g, f(**{n: base[n] + 8}), -3, "aligned")
+    for n in ("beta", "gate", "offsets", "dbeta", "dgate"):
+        expect(g, f(**{n: base[n] + 2}), -3, "aligned")
+    expect(g, f(ws=None), -5, "NULL")
+    expect(g, f(bytes=1 << 20), -5, "needed")
+    expect(g, f(ws=base["ws"] + 4), -3, "workspace")
+    for n in ("dq", "dk", "dv", "dbeta", "dgate", "d_state"):
+        for m in BACK:
+            if m != n and (n, m) != ("d_state", "d_state_out"):
+                expect(g, f(**{n: base[m]}), -4, "overlaps")
+        expect(g, f(**{n: base["ws"] + 1024}), -4, "overlaps")
+    expect(g, f(d_state=base["d_state_out"] + 16), -4, "d_state")
+
+
+def test_backward_workspace_bytes(g):
+    f = g.chunk_backward_workspace_bytes
+    d = g.Dims(4, 2, 128, 128)
+    assert 0 < f(1, 1, torch.bfloat16, d) < f(1, 200, torch.bfloat16, d) < f(1, 200, torch.float32, d)
+    assert f(0, 1, torch.bfloat16, d) == 0 and f(1, 1, torch.int8, d) == 0
