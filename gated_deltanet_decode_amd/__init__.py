@@ -37,6 +37,9 @@ C entry points:
     chunk_backward_workspace_bytes(B, tokens, dtype)
                                                  -> gdn_chunk_backward_workspace_bytes
     decode(q, k, v, beta, gate, out, state, state_out, offsets, slots) -> gdn_decode
+    logprobs(logits, tokens, logprob, entropy, top_ids, top_logprobs, workspace)
+                                                 -> gdn_logprobs
+    logprobs_workspace_bytes(rows, V, top)       -> gdn_logprobs_workspace_bytes
     last_error(), version()
 
 If the library has not been built, importing this package raises: there is
@@ -56,7 +59,8 @@ __all__ = ["GdnError", "Dims", "TailParams", "GateInputs", "lib", "step", "bind_
            "layer_tail_ba",
            "layer_tail_ba_workspace_bytes", "add_rmsnorm_q8", "quantize_q8", "linear_q8",
            "verify", "verify_workspace_bytes", "pair_commit", "chunk", "chunk_workspace_bytes",
-           "chunk_backward", "chunk_backward_workspace_bytes", "decode", "last_error", "version", "PAGE_DIMS",
+           "chunk_backward", "chunk_backward_workspace_bytes", "decode",
+           "logprobs", "logprobs_workspace_bytes", "last_error", "version", "PAGE_DIMS",
            "PAGE_TAIL", "ERRORS"]
 
 if not os.path.exists(LIBRARY):
@@ -163,6 +167,11 @@ lib.gdn_chunk_backward_workspace_bytes.restype = ctypes.c_size_t
 lib.gdn_chunk_backward_workspace_bytes.argtypes = [_DP] + [_i32] * 3
 lib.gdn_decode.restype = ctypes.c_int
 lib.gdn_decode.argtypes = [_DP] + [_i32] * 3 + [_vp] * 7 + [_i32] + [_vp] * 3 + [_vp]
+lib.gdn_logprobs.restype = ctypes.c_int
+lib.gdn_logprobs.argtypes = [_i32, _i32, ctypes.c_int64, _i32] + [_vp] * 4 + [_i32] + [_vp] * 2 + \
+    [_vp, ctypes.c_size_t, _vp]
+lib.gdn_logprobs_workspace_bytes.restype = ctypes.c_size_t
+lib.gdn_logprobs_workspace_bytes.argtypes = [_i32] * 3
 
 
 class GdnError(RuntimeError):
@@ -751,3 +760,38 @@ def decode(q, k, v, beta, gate, out, state, state_out=None, offsets=None, slots=
            (ctypes.byref(d), *args,
             *_states(state, state if state_out is None else state_out, slots, args[0], d, dev),
             _addr(out, "out", q.dtype, vs, dev)), dev, stream)
+
+
+def logprobs_workspace_bytes(rows: int, V: int, top: int = 0) -> int:
+    if not (0 < rows <= _INT32_MAX and 0 < V <= _INT32_MAX and 0 <= top <= _INT32_MAX):
+        return 0
+    return int(lib.gdn_logprobs_workspace_bytes(rows, V, top))
+
+
+def logprobs(logits, tokens=None, logprob=None, entropy=None, top_ids=None, top_logprobs=None,
+             workspace=None, stream=None) -> None:
+    """gdn_logprobs: logits [rows][V] of float32, bfloat16 or float16, whose rows
+    may lie apart (a slice of a padded vocabulary); tokens [rows] int32 with
+    logprob [rows] float32, entropy [rows] float32, and top_ids [rows][top] int32
+    with top_logprobs [rows][top] float32, each None where it is not wanted.
+    workspace: a GPU tensor of at least logprobs_workspace_bytes(rows, V, top)
+    bytes."""
+    dev = _lead(logits, "logits", 2, _TYPES)
+    rows, V = logits.shape
+    ld, step = logits.stride()
+    if step != 1 and V > 1 or ld < V and rows > 1:
+        raise ValueError(f"logits has strides {(ld, step)}: entries of a row must be neighbours "
+                         "and rows must not overlap")
+    top = 0
+    if top_ids is not None or top_logprobs is not None:
+        _lead(top_ids, "top_ids", 2)
+        top = top_ids.shape[1]
+    w = (rows,)
+    _issue(lib.gdn_logprobs,
+           (rows, V, max(ld, V), _TYPES[logits.dtype], logits.data_ptr(),
+            None if tokens is None else _addr(tokens, "tokens", _I32, w, dev),
+            None if logprob is None else _addr(logprob, "logprob", _F32, w, dev),
+            None if entropy is None else _addr(entropy, "entropy", _F32, w, dev), top,
+            None if top == 0 else _addr(top_ids, "top_ids", _I32, (rows, top), dev),
+            None if top == 0 else _addr(top_logprobs, "top_logprobs", _F32, (rows, top), dev),
+            *_scratch(workspace, dev)), dev, stream)

@@ -1,5 +1,5 @@
 // gdn_check.hpp - argument checks and error reporting shared by the C-ABI
-// sources (gdn_api.cpp, gdn_serve_api.cpp, gdn_chunk_api.cpp, gdn_f8_api.cpp).  All validation happens on the
+// sources (gdn_*api.cpp).  All validation happens on the
 // host before anything is enqueued.
 #pragma once
 

@@ -587,6 +587,41 @@ int gdn_decode(const gdn_dims *dims, int32_t B, int32_t tokens, int32_t type, co
                const int32_t *offsets, const int32_t *slots, int32_t n_slots, const float *state,
                float *state_out, void *out, void *stream);
 
+/*
+ * gdn_logprobs - log probabilities of the answer: of one given token a row, the
+ * row's entropy and its `top` most likely tokens, from logits (beside
+ * gdn_verify, whose tokens have a row of logits each).  With m the largest
+ * logit of a row and Z = sum exp(x - m):
+ *   logprob = x[token] - m - log Z,  entropy = -sum p log p  (natural logarithms).
+ * Z and the entropy's sum are float32 within a thread and binary64 across them;
+ * the results round once.  Entries of -inf have probability 0 (a masked
+ * vocabulary).  A row of nothing else gets logprob -inf and entropy 0; a row with
+ * a NaN or +inf gets NaN, and -1 for the ids.
+ *   logits       rows of V entries of logit_type, ld >= V elements apart (a padded
+ *                vocabulary is not read)
+ *   tokens       [rows]       int32, optional; one outside [0, V) has logprob -inf
+ *   logprob      [rows]       float32, given exactly when tokens is
+ *   entropy      [rows]       float32, optional
+ *   top_ids      [rows][top]  int32: by logit descending, equal ones by id
+ *   top_logprobs [rows][top]  float32
+ *                             ascending; both ignored where top is 0
+ *   workspace    gdn_logprobs_workspace_bytes(rows, V, top) bytes, 16-byte
+ *                aligned; NULL where that is 0.  Two calls that may overlap in
+ *                time need one each.
+ * Alignment: logits one element, the others 4 bytes.  Limits (GDN_ERR_SHAPE
+ * beyond): 1 <= rows <= 4194303, 1 <= V <= 2^30, ld <= 2^40,
+ * 0 <= top <= min(GDN_LOGPROBS_MAX_TOP, V).
+ */
+#define GDN_LOGPROBS_MAX_TOP 64
+int gdn_logprobs(int32_t rows, int32_t V, int64_t ld, int32_t logit_type, const void *logits,
+                 const int32_t *tokens, float *logprob, float *entropy, int32_t top,
+                 int32_t *top_ids, float *top_logprobs, void *workspace, size_t workspace_bytes,
+                 void *stream);
+
+/* Bytes of workspace gdn_logprobs needs (0 on invalid arguments, and where it needs
+ * none). */
+size_t gdn_logprobs_workspace_bytes(int32_t rows, int32_t V, int32_t top);
+
 /* Message for the last non-zero return on this thread ("" if none). */
 const char *gdn_last_error(void);
 
