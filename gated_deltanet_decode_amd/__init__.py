@@ -37,6 +37,8 @@ C entry points:
     chunk_backward_workspace_bytes(B, tokens, dtype)
                                                  -> gdn_chunk_backward_workspace_bytes
     decode(q, k, v, beta, gate, out, state, state_out, offsets, slots) -> gdn_decode
+    quantize_f8(x, q, scale, block_rows)         -> gdn_quantize_f8
+    linear_f8(a, a_scale, w, w_scale, outs)      -> gdn_linear_f8
     logprobs(logits, tokens, logprob, entropy, top_ids, top_logprobs, workspace)
                                                  -> gdn_logprobs
     logprobs_workspace_bytes(rows, V, top)       -> gdn_logprobs_workspace_bytes
@@ -60,7 +62,7 @@ __all__ = ["GdnError", "Dims", "TailParams", "GateInputs", "lib", "step", "bind_
            "layer_tail_ba_workspace_bytes", "add_rmsnorm_q8", "quantize_q8", "linear_q8",
            "verify", "verify_workspace_bytes", "pair_commit", "chunk", "chunk_workspace_bytes",
            "chunk_backward", "chunk_backward_workspace_bytes", "decode",
-           "logprobs", "logprobs_workspace_bytes", "last_error", "version", "PAGE_DIMS",
+           "quantize_f8", "linear_f8", "logprobs", "logprobs_workspace_bytes", "last_error", "version", "PAGE_DIMS",
            "PAGE_TAIL", "ERRORS"]
 
 if not os.path.exists(LIBRARY):
@@ -167,6 +169,10 @@ lib.gdn_chunk_backward_workspace_bytes.restype = ctypes.c_size_t
 lib.gdn_chunk_backward_workspace_bytes.argtypes = [_DP] + [_i32] * 3
 lib.gdn_decode.restype = ctypes.c_int
 lib.gdn_decode.argtypes = [_DP] + [_i32] * 3 + [_vp] * 7 + [_i32] + [_vp] * 3 + [_vp]
+lib.gdn_quantize_f8.restype = ctypes.c_int
+lib.gdn_quantize_f8.argtypes = [_i32] * 4 + [_vp] * 4
+lib.gdn_linear_f8.restype = ctypes.c_int
+lib.gdn_linear_f8.argtypes = lib.gdn_linear_q8.argtypes
 lib.gdn_logprobs.restype = ctypes.c_int
 lib.gdn_logprobs.argtypes = [_i32, _i32, ctypes.c_int64, _i32] + [_vp] * 4 + [_i32] + [_vp] * 2 + \
     [_vp, ctypes.c_size_t, _vp]
@@ -457,9 +463,9 @@ def layer_tail_ba(x, conv_w, conv_state, ba, a_log, dt_bias, state, z, norm_w, y
 # the stream given, which must be that GPU's) whichever GPU is current.
 try:
     _TYPES = {_torch.float32: 0, _torch.bfloat16: 1, _torch.float16: 2}
-    _I8, _I32 = _torch.int8, _torch.int32
+    _I8, _I32, _F8 = _torch.int8, _torch.int32, _torch.float8_e4m3fn
 except NameError:
-    _TYPES, _I8, _I32 = {}, None, None
+    _TYPES, _I8, _I32, _F8 = {}, None, None, None
 _NO_TYPE = -1
 _INT32_MAX = 2 ** 31 - 1
 
@@ -558,13 +564,8 @@ def quantize_q8(x, q, scale, stream=None) -> None:
            dev, stream)
 
 
-def linear_q8(a, a_scale, w, w_scale, outs, bias=None, stream=None) -> None:
-    """gdn_linear_q8: a [M][K] int8 with a_scale [M], w [N][K] int8 with w_scale
-    [N] (bias [N] float32 or None) -> outs: a tensor [M][N], or up to four
-    [M][n_i] that take the N channels in order; float32, bfloat16 or float16,
-    all of one type."""
-    dev = _lead(a, "a", 2)
-    M, K = a.shape
+def _linear_outs(outs, M, dev):
+    """outs of linear_q8 and linear_f8: type, groups and the number of channels."""
     if not isinstance(outs, (list, tuple)):
         outs = (outs,)
     if not 1 <= len(outs) <= LINEAR_MAX_OUTS:
@@ -580,12 +581,22 @@ def linear_q8(a, a_scale, w, w_scale, outs, bias=None, stream=None) -> None:
         n = o.shape[1]
         addrs.append((_addr(o, name, dtype, (M, n), dev), n))
         N += n
-    groups = _GROUPS[len(outs)](*addrs)
+    return dtype, _GROUPS[len(outs)](*addrs), len(outs), N
+
+
+def linear_q8(a, a_scale, w, w_scale, outs, bias=None, stream=None) -> None:
+    """gdn_linear_q8: a [M][K] int8 with a_scale [M], w [N][K] int8 with w_scale
+    [N] (bias [N] float32 or None) -> outs: a tensor [M][N], or up to four
+    [M][n_i] that take the N channels in order; float32, bfloat16 or float16,
+    all of one type."""
+    dev = _lead(a, "a", 2)
+    M, K = a.shape
+    dtype, groups, n_outs, N = _linear_outs(outs, M, dev)
     _issue(lib.gdn_linear_q8,
            (M, K, _addr(a, "a", _I8, (M, K), dev), _addr(a_scale, "a_scale", _F32, (M,), dev),
             _addr(w, "w", _I8, (N, K), dev), _addr(w_scale, "w_scale", _F32, (N,), dev),
             None if bias is None else _addr(bias, "bias", _F32, (N,), dev),
-            _TYPES[dtype], groups, len(outs)), dev, stream)
+            _TYPES[dtype], groups, n_outs), dev, stream)
 
 
 def verify_workspace_bytes(B: int, V: int) -> int:
@@ -760,6 +771,35 @@ def decode(q, k, v, beta, gate, out, state, state_out=None, offsets=None, slots=
            (ctypes.byref(d), *args,
             *_states(state, state if state_out is None else state_out, slots, args[0], d, dev),
             _addr(out, "out", q.dtype, vs, dev)), dev, stream)
+
+
+def quantize_f8(x, q, scale, block_rows=1, stream=None) -> None:
+    """gdn_quantize_f8: x [rows][n] of float32, bfloat16 or float16 -> codes q
+    [rows][n] float8_e4m3fn and scale [rows][ceil(n / 128)] float32; with
+    block_rows=128 (weights) scale [ceil(rows / 128)][ceil(n / 128)]."""
+    dev = _lead(x, "x", 2, _TYPES)
+    rows, n = shape = x.shape
+    tall = rows if block_rows == 1 else (rows + 127) // 128
+    _issue(lib.gdn_quantize_f8,
+           (rows, n, block_rows, _TYPES[x.dtype], _addr(x, "x", x.dtype, shape, dev),
+            _addr(q, "q", _F8, shape, dev), _addr(scale, "scale", _F32, (tall, (n + 127) // 128), dev)),
+           dev, stream)
+
+
+def linear_f8(a, a_scale, w, w_scale, outs, bias=None, stream=None) -> None:
+    """gdn_linear_f8: a [M][K] float8_e4m3fn with a_scale [M][ceil(K / 128)], w
+    [N][K] float8_e4m3fn with w_scale [ceil(N / 128)][ceil(K / 128)] (bias [N]
+    float32 or None) -> outs as in linear_q8."""
+    dev = _lead(a, "a", 2)
+    M, K = a.shape
+    dtype, groups, n_outs, N = _linear_outs(outs, M, dev)
+    kb = (K + 127) // 128
+    _issue(lib.gdn_linear_f8,
+           (M, K, _addr(a, "a", _F8, (M, K), dev), _addr(a_scale, "a_scale", _F32, (M, kb), dev),
+            _addr(w, "w", _F8, (N, K), dev),
+            _addr(w_scale, "w_scale", _F32, ((N + 127) // 128, kb), dev),
+            None if bias is None else _addr(bias, "bias", _F32, (N,), dev),
+            _TYPES[dtype], groups, n_outs), dev, stream)
 
 
 def logprobs_workspace_bytes(rows: int, V: int, top: int = 0) -> int:

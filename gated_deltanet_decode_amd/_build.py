@@ -14,7 +14,8 @@ SOURCES = [os.path.join(CSRC, f) for f in
            ("gdn_api.cpp", "gdn_step.hip", "gdn_seq.hip", "gdn_tail.hip",
             "gdn_serve_api.cpp", "gdn_quant.hip", "gdn_linear.hip", "gdn_verify.hip",
             "gdn_chunk_api.cpp", "gdn_chunk.hip", "gdn_chunk_back.hip", "gdn_decode.hip",
-            "gdn_logprobs_api.cpp", "gdn_logprobs.hip")]
+            "gdn_logprobs_api.cpp", "gdn_logprobs.hip",
+            "gdn_f8_api.cpp", "gdn_quant_f8.hip", "gdn_linear_f8.hip")]
 # Measurement aids (a copy of known size and an in-place read-modify-write with
 # the step kernel's access pattern), built as their own library.
 PROBE_LIBRARY = os.path.join(CSRC, "libgdn_probe.so")

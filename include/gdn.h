@@ -588,6 +588,47 @@ int gdn_decode(const gdn_dims *dims, int32_t B, int32_t tokens, int32_t type, co
                float *state_out, void *out, void *stream);
 
 /*
+ * gdn_quantize_f8 - 8-bit floating point codes (e4m3: one sign, four exponent and
+ * three mantissa bits, largest value 448, no infinities) with one scale for each
+ * block of 128 elements of a row (block_rows 1: activations) or of 128 rows by 128
+ * elements (block_rows 128: weights, laid out once).  With G the block's
+ * largest magnitude,
+ *   scale = G / 448 (rounded once),  q = 448 x / G rounded to e4m3, ties to even,
+ * of the exact quotient.  A block of zeros gets q = 0 and scale = 0; one with a
+ * NaN or an infinity q = 0 and scale = NaN.  The last blocks may be smaller.
+ *   x      [rows][n]  of x_type
+ *   q      [rows][n]  bytes, output
+ *   scale  [rows or ceil(rows / 128)][ceil(n / 128)]  float32, output
+ * Pointer alignment: 16 bytes, scale 4.  Limits (GDN_ERR_SHAPE beyond): rows,
+ * n >= 1, n <= 1073741823, and at most 536870880 scales (block_rows 128:
+ * 16777215).
+ */
+int gdn_quantize_f8(int32_t rows, int32_t n, int32_t block_rows, int32_t x_type, const void *x,
+                    uint8_t *q, float *scale, void *stream);
+
+/*
+ * gdn_linear_f8 - product of e4m3 rows with e4m3 weights under block scales:
+ *   y[m][c] = sum_b a_scale[m][b] w_scale[c / 128][b] (sum_{k in b} a[m][k] w[c][k])
+ *             + bias[c],  b the blocks of 128 k (the last may be smaller).
+ * All sums are float32 and y rounds once to out_type.  For out_type GDN_F32 the
+ * codes are widened to fp16 (exact) and a block's sum is right to float32; for
+ * 16-bit outputs it comes from the 8-bit matrix instructions, which drop what
+ * lies about 2^-16 below a sum's largest product.  The order of the blocks'
+ * sums depends on M, N and K; the same call gives the same bits.
+ *   a        [M][K]  e4m3 bytes   a_scale  [M][ceil(K / 128)]              float32
+ *   w        [N][K]  e4m3 bytes   w_scale  [ceil(N / 128)][ceil(K / 128)]  float32
+ *   bias     [N]     float32, optional (NULL = none)
+ *   outs     n_outs groups that take the N channels in order, as in gdn_linear_q8
+ *            (w_scale's blocks count through all N channels)
+ * Pointer alignment: a, w and the outputs 16 bytes, the float32 vectors 4.
+ * Limits (GDN_ERR_SHAPE beyond): M >= 1, 1 <= K <= 4194303,
+ * 1 <= N <= 134217727, and ceil(M / 64) * ceil(N / 64) <= 4194303.
+ */
+int gdn_linear_f8(int32_t M, int32_t K, const uint8_t *a, const float *a_scale, const uint8_t *w,
+                  const float *w_scale, const float *bias, int32_t out_type,
+                  const gdn_linear_out *outs, int32_t n_outs, void *stream);
+
+/*
  * gdn_logprobs - log probabilities of the answer: of one given token a row, the
  * row's entropy and its `top` most likely tokens, from logits (beside
  * gdn_verify, whose tokens have a row of logits each).  With m the largest
