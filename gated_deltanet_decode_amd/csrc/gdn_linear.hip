@@ -532,20 +532,6 @@ __global__ __launch_bounds__(64 * WN * WM) void k_linear_block(LinearArgs a, int
 // k is a multiple of 256 here: masks for a ragged k did not fit beside operands
 // held ahead, and one half at a time was 15-75 % slower than rounds of 256 x 128
 // tiles (124 us against 89 at 4096 x 8192 x 2176 into f32).
-struct Tile {
-    int n, m;
-};
-// Tile i in an order that keeps neighbours close: groups of 8 token tiles by
-// all channel tiles.
-__device__ __forceinline__ Tile tile_at(int i, int tiles_n, int tiles_m) {
-    constexpr int kG = 8;
-    const int per = kG * tiles_n;
-    const int grp = i / per, in = i - grp * per;
-    const int gm = min(kG, tiles_m - grp * kG);
-    const int n = in / gm;
-    return Tile{__builtin_amdgcn_readfirstlane(n), __builtin_amdgcn_readfirstlane(grp * kG + in - n * gm)};
-}
-
 template <typename OT>
 __global__ __launch_bounds__(512) void k_linear_tile(LinearArgs a, int tiles_n, int tiles_m) {
     constexpr int BN = 256, BM = 256, WN = 4, NW = 8;

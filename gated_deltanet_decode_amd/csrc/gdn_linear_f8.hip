@@ -23,6 +23,8 @@
 #include "gdn_launch.hpp"
 #include "gdn_tile.hpp"
 
+#include <type_traits>
+
 namespace gdn {
 namespace {
 
@@ -60,33 +62,47 @@ __device__ __forceinline__ f4 mul(const Halfs &w, const Halfs &x) {
     return c;
 }
 
+// A block's sum on its way from the matrix unit: it joins the running sum while the
+// next one is formed.  (Joined at once, every sum's latency is waited for.)
+__device__ __forceinline__ void in_order() {              // nothing passes: reads hoisted above would hold registers
+    __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ void join(f4 &acc, const f4 &p, float s) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] = fmaf(p[e], s, acc[e]);
+}
+
 // All TN x TM tiles of a wave over one block of k; s: the scales' product per token
-// tile.
-template <bool kWide, int TN, int TM>
-__device__ __forceinline__ void mul_block(const Codes (&w)[TN], const Codes (&x)[TM], const float (&s)[TM], f4 (&acc)[TN][TM]) {
-    if constexpr (kWide) {
-        Halfs xh[TM];
+// tile.  done(i): the weights of channel tile i are not needed any more.
+template <bool kWide, int TN, int TM, typename F>
+__device__ __forceinline__ void mul_block(const Codes (&w)[TN], const Codes (&x)[TM], const float (&s)[TM],
+                                          f4 (&acc)[TN][TM], F done) {
+    typedef typename std::conditional<kWide, Halfs, Codes>::type Operand;
+    const auto operand = [](const Codes &c) {
+        if constexpr (kWide) return widen(c);
+        else return c;
+    };
+    Operand xo[TM];
 #pragma unroll
-        for (int j = 0; j < TM; ++j) xh[j] = widen(x[j]);
+    for (int j = 0; j < TM; ++j) xo[j] = operand(x[j]);
+    f4 p[2];                                              // two sums are on their way while one joins
+    Operand wo;
 #pragma unroll
-        for (int i = 0; i < TN; ++i) {
-            const Halfs wh = widen(w[i]);
-#pragma unroll
-            for (int j = 0; j < TM; ++j) {
-                const f4 p = mul(wh, xh[j]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], s[j], acc[i][j][e]);
+    for (int t = 0; t < TN * TM + 2; ++t) {
+        const int i = t / TM, j = t % TM, k = t - 2;
+        f4 q = {};
+        if (t < TN * TM) {
+            if (j == 0) {
+                wo = operand(w[i]);
+                if (kWide) done(i);
             }
+            q = mul(wo, xo[j]);
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < TN; ++i)
-#pragma unroll
-            for (int j = 0; j < TM; ++j) {
-                const f4 p = mul(w[i], x[j]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], s[j], acc[i][j][e]);
-            }
+        in_order();
+        if (t > 1) join(acc[k / TM][k % TM], p[t % 2], s[k % TM]);
+        in_order();
+        p[t % 2] = q;
+        if (!kWide && t < TN * TM && j == TM - 1) done(i);
     }
 }
 
@@ -136,16 +152,84 @@ struct Scales {
     }
 };
 
+// A row's codes in LDS; codes past the last k cleared in both operands (a stray one
+// could be a NaN), `left` of k from the block's start on.
+__device__ __forceinline__ Codes codes_at(const int8_t *p, const int (&rd)[2]) {
+    return Codes{*reinterpret_cast<const i4 *>(p + rd[0]), *reinterpret_cast<const i4 *>(p + rd[1])};
+}
+template <int TN, int TM>
+__device__ __forceinline__ void clear_past(int left, int g, Codes (&w)[TN], Codes (&x)[TM]) {
+    const bool lo = 16 * g < left, hi = 64 + 16 * g < left;
+    const i4 zero = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < TN; ++i) w[i] = Codes{lo ? w[i].lo : zero, hi ? w[i].hi : zero};
+#pragma unroll
+    for (int j = 0; j < TM; ++j) x[j] = Codes{lo ? x[j].lo : zero, hi ? x[j].hi : zero};
+}
+
+// Writes a wave's TN x TM matrix tiles.  Where all its channels belong to one group
+// they pass through the wave's own piece of LDS, 16 tokens at a time, so that a
+// store covers whole lines of a token's row.
+constexpr int kStageBytes = 4096;
+template <typename OT, int TN, int TM>
+__device__ __forceinline__ void write_tile(const LinearF8Args &a, int c0, int m0, int lane, int8_t *stage,
+                                           const f4 (&acc)[TN][TM]) {
+    typedef typename OT::bits bits;
+    const int r = lane & 15, g = lane >> 4;
+    int first;
+    const int s = group_of(a, c0, first);
+    if (c0 + TN * 16 > a.end[s]) {                        // several groups, or the last channels
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+            for (int j = 0; j < TM; ++j) put4<OT>(a, c0 + 16 * i + 4 * g, m0 + 16 * j + r, acc[i][j]);
+        return;
+    }
+    const int n = a.end[s] - first;
+    bits *out = static_cast<bits *>(a.out[s]) + static_cast<int64_t>(m0) * n + (c0 - first);
+    f4 bias[TN];
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+        bias[i] = a.bias ? Pack<float, 4>::load(a.bias + c0 + i * 16 + 4 * g) : f4{0, 0, 0, 0};
+    constexpr int kRow = TN * 16 * sizeof(bits);          // bytes of a token's channels
+    constexpr int kLanes = kRow / 16;                     // lanes that store a token's row
+    static_assert(16 * kRow <= kStageBytes && (kLanes & (kLanes - 1)) == 0 && kLanes >= 4, "stage");
+    // chunk c (16 bytes) of row i lies at c ^ (i modulo the chunks)
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+#pragma unroll
+        for (int i = 0; i < TN; ++i) {
+            typename Pack<bits, 4>::vec v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = OT::put(acc[i][j][e] + bias[i][e]);
+            const int at = (i * 16 + 4 * g) * sizeof(bits);
+            *reinterpret_cast<typename Pack<bits, 4>::vec *>(stage + r * kRow + (((at >> 4) ^ (r & (kLanes - 1))) << 4) +
+                                                             (at & 15)) = v;
+        }
+#pragma unroll
+        for (int p = 0; p < 16 * kLanes / 64; ++p) {
+            const int row = p * (64 / kLanes) + lane / kLanes, col = lane % kLanes;
+            const i4 v = *reinterpret_cast<const i4 *>(stage + row * kRow + 16 * (col ^ (row & (kLanes - 1))));
+            const int m = j * 16 + row;
+            if (m0 + m < a.M)
+                Pack<bits, 16 / sizeof(bits)>::store(out + static_cast<int64_t>(m) * n + col * (16 / sizeof(bits)),
+                                                     __builtin_bit_cast(typename Pack<bits, 16 / sizeof(bits)>::vec, v));
+        }
+    }
+}
+
 // ------------------------------------------------------------- split product
 // For few tokens: a workgroup's WK waves share one tile of 16 TN channels x 16 TM
 // tokens and split the blocks of k among them, each with a ring of S blocks of
-// its own in LDS.  The partial sums meet in LDS.
+// its own in LDS (separate arrays: a read of one does not wait for the fetches of
+// another).  The partial sums meet in LDS.
 template <int TN, int TM, int WK, int S, bool kVec, bool kWide>
 __global__ __launch_bounds__(64 * WK) void k_f8_ring(LinearF8Args a, int tiles_n, int tiles_m) {
     constexpr int L = 2 * (TN + TM);
     constexpr int kPiece = L * 1024;
-    static_assert(TN * TM * 1024 <= S * kPiece, "the sums fit a wave's ring");
-    __shared__ alignas(1024) int8_t ring[WK][S][kPiece];
+    static_assert(S >= 2 && S <= 4 && (S - 1) * L < 60 && TN * TM <= L, "");
+    __shared__ alignas(1024) int8_t r0[WK * kPiece], r1[kVec ? WK * kPiece : 16], r2[kVec && S > 2 ? WK * kPiece : 16],
+        r3[kVec && S > 3 ? WK * kPiece : 16];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
@@ -171,87 +255,107 @@ __global__ __launch_bounds__(64 * WK) void k_f8_ring(LinearF8Args a, int tiles_n
     const float *sw = a.w_scale + static_cast<int64_t>(c0 / kF8Block) * blocks;
     f4 acc[TN][TM] = {};
     Codes w[TN], x[TM];
+    float s[TM];
     auto read = [&](const int8_t *piece) {
 #pragma unroll
-        for (int i = 0; i < TN; ++i)
-            w[i] = Codes{*reinterpret_cast<const i4 *>(piece + i * 2048 + rd[0]), *reinterpret_cast<const i4 *>(piece + i * 2048 + rd[1])};
+        for (int i = 0; i < TN; ++i) w[i] = codes_at(piece + i * 2048, rd);
 #pragma unroll
-        for (int j = 0; j < TM; ++j)
-            x[j] = Codes{*reinterpret_cast<const i4 *>(piece + (TN + j) * 2048 + rd[0]),
-                         *reinterpret_cast<const i4 *>(piece + (TN + j) * 2048 + rd[1])};
+        for (int j = 0; j < TM; ++j) x[j] = codes_at(piece + (TN + j) * 2048, rd);
     };
-    // Codes past the last k are zero in both operands (a stray one could be a NaN).
-    auto mask = [&](int left) {
-        const bool lo = 16 * g < left, hi = 64 + 16 * g < left;
-        const i4 zero = {0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < TN; ++i) w[i] = Codes{lo ? w[i].lo : zero, hi ? w[i].hi : zero};
-#pragma unroll
-        for (int j = 0; j < TM; ++j) x[j] = Codes{lo ? x[j].lo : zero, hi ? x[j].hi : zero};
-    };
-    float s[TM];
+    int8_t *const p0 = r0 + wave * kPiece;
     if constexpr (kVec) {
-        auto fetch = [&](int slot, int i) {               // past the end: the last block again
+        int8_t *const p1 = r1 + wave * kPiece, *const p2 = S > 2 ? r2 + wave * kPiece : nullptr,
+                     *const p3 = S > 3 ? r3 + wave * kPiece : nullptr;
+        auto fetch = [&](int8_t *piece, int i) {          // past the end: the last block again
             const int k0 = (wave + min(i, n - 1) * WK) * kBK;
 #pragma unroll
             for (int j = 0; j < L; ++j)
-                fetch16(ring[wave][slot] + j * 1024, j < 2 * TN ? pw : px, j < 2 * TN ? nw : nx, off[j], k0);
+                fetch16(piece + j * 1024, j < 2 * TN ? pw : px, j < 2 * TN ? nw : nx, off[j], k0);
         };
-        auto step = [&](int slot, int i) {
+        auto step = [&](int8_t *piece, int i) {
             const int b = wave + i * WK;
+            wait_mem<(S - 1) * L, false>();               // block i has landed
             sc.at(b, sw[b], s);
-            wait_mem<0, false>();
-            read(ring[wave][slot]);
-            wait_mem<63, true>();
-            fetch(slot, i + S);
-            if ((b + 1) * kBK > a.K) mask(a.K - b * kBK);
-            mul_block<kWide>(w, x, s, acc);
+            read(piece);
+            wait_mem<63, true>();                         // and is in registers: its piece is free
+            fetch(piece, i + S);
+            if ((b + 1) * kBK > a.K) clear_past(a.K - b * kBK, g, w, x);
+            mul_block<kWide>(w, x, s, acc, [](int) {});
+            __builtin_amdgcn_sched_barrier(0);            // registers do not live over two steps
         };
         if (n > 0) {
-            for (int i = 0; i < S; ++i) fetch(i, i);
-            for (int i = 0, slot = 0; i < n; ++i, slot = slot + 1 == S ? 0 : slot + 1) step(slot, i);
+            fetch(p0, 0);
+            fetch(p1, 1);
+            if constexpr (S > 2) fetch(p2, 2);
+            if constexpr (S > 3) fetch(p3, 3);
+            // whole rounds of the ring, then what is left (a branch out of a round
+            // would make the compiler wait for every fetch where the paths meet)
+            int i = 0;
+            for (; i + S <= n; i += S) {
+                step(p0, i);
+                step(p1, i + 1);
+                if constexpr (S > 2) step(p2, i + 2);
+                if constexpr (S > 3) step(p3, i + 3);
+            }
+            if (i < n) {
+                step(p0, i);
+                if constexpr (S > 2)
+                    if (i + 1 < n) {
+                        step(p1, i + 1);
+                        if constexpr (S > 3)
+                            if (i + 2 < n) step(p2, i + 2);
+                    }
+            }
         }
         wait_mem<0, true>();
     } else {
+        // whole blocks one ahead in registers, the one past them by itself
+        const int whole = (a.K / kBK - wave + WK - 1) / WK;
         i4 v[L];
         auto load = [&](int i) {
             const int k0 = (wave + i * WK) * kBK;
 #pragma unroll
-            for (int j = 0; j < L; ++j)
-                v[j] = (k0 + kBK <= a.K) ? any16((j < 2 * TN ? pw : px) + off[j] + k0 + at[j])
-                                         : load16((j < 2 * TN ? pw : px) + off[j], k0 + at[j], a.K, j < 2 * TN ? we : xe);
+            for (int j = 0; j < L; ++j) v[j] = any16((j < 2 * TN ? pw : px) + off[j] + k0 + at[j]);
         };
-        if (n > 0) load(0);
-        for (int i = 0; i < n; ++i) {
+        auto step = [&](int i, bool more) {
 #pragma unroll
-            for (int j = 0; j < L; ++j) *reinterpret_cast<i4 *>(ring[wave][0] + j * 1024 + lane * 16) = v[j];
+            for (int j = 0; j < L; ++j) *reinterpret_cast<i4 *>(p0 + j * 1024 + lane * 16) = v[j];
             const int b = wave + i * WK;
             sc.at(b, sw[b], s);
-            if (i + 1 < n) load(i + 1);
-            read(ring[wave][0]);
-            mul_block<kWide>(w, x, s, acc);
+            if (more) load(i + 1);
+            read(p0);
+            mul_block<kWide>(w, x, s, acc, [](int) {});
+        };
+        if (whole > 0) load(0);
+        for (int i = 0; i < whole; ++i) step(i, i + 1 < whole);
+        if (whole < n) {
+            const int k0 = (wave + whole * WK) * kBK;
+#pragma unroll
+            for (int j = 0; j < L; ++j)
+                v[j] = load16((j < 2 * TN ? pw : px) + off[j], k0 + at[j], a.K, j < 2 * TN ? we : xe);
+            step(whole, false);
         }
     }
-    // a wave's sums lie in its own ring, in its own lanes' order
-    int8_t *const mine = ring[wave][0];
+    // a wave's sums lie in its own piece, in its own lanes' order
 #pragma unroll
-    for (int t = 0; t < TN * TM; ++t) *reinterpret_cast<f4 *>(mine + t * 1024 + lane * 16) = acc[t / TM][t % TM];
+    for (int t = 0; t < TN * TM; ++t) *reinterpret_cast<f4 *>(p0 + t * 1024 + lane * 16) = acc[t / TM][t % TM];
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < (TN * TM + WK - 1) / WK; ++i) {
         const int t = wave + i * WK;
         if (t >= TN * TM) break;
-        f4 y = *reinterpret_cast<const f4 *>(ring[0][0] + t * 1024 + lane * 16);
+        f4 y = *reinterpret_cast<const f4 *>(r0 + t * 1024 + lane * 16);
 #pragma unroll
-        for (int k = 1; k < WK; ++k) y += *reinterpret_cast<const f4 *>(ring[k][0] + t * 1024 + lane * 16);
+        for (int k = 1; k < WK; ++k) y += *reinterpret_cast<const f4 *>(r0 + k * kPiece + t * 1024 + lane * 16);
         put4(a, c0 + 16 * (t / TM) + 4 * g, m0 + 16 * (t % TM) + r, y);
     }
 }
 
 // ------------------------------------------------------- one tile a workgroup
 // BN channels x BM tokens a workgroup, its waves in a WN x WM grid over them, a ring
-// of S blocks in LDS.  While a block is multiplied the next one is read from
-// LDS; one barrier a block hands its buffer back to the fetches.
+// of S blocks in LDS; one barrier a block hands its buffer back to the fetches.
+// While a block is multiplied the next one is read from LDS: its tokens into a second
+// set of registers, its weights, one tile after another, into those that are done.
 template <typename OT, int BN, int BM, int WN, int WM, int S, bool kVec, bool kWide>
 __global__ __launch_bounds__(64 * WN * WM) void k_f8_block(LinearF8Args a, int tiles_n, int tiles_m) {
     constexpr int NW = WN * WM;
@@ -259,7 +363,8 @@ __global__ __launch_bounds__(64 * WN * WM) void k_f8_block(LinearF8Args a, int t
     constexpr int L = (BN + BM) / 8 / NW, LN = BN / 8 / NW;
     constexpr int kBytes = (BN + BM) * kBK;
     static_assert(kF8Block % (16 * TN) == 0, "a wave's channels share a scale");
-    __shared__ alignas(1024) int8_t ring[S][kBytes];
+    static_assert((S == 2 || S == 4) && NW * kStageBytes <= kBytes, "");
+    __shared__ alignas(1024) int8_t r0[kBytes], r1[kBytes], r2[S > 2 ? kBytes : 16], r3[S > 2 ? kBytes : 16];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
@@ -268,17 +373,20 @@ __global__ __launch_bounds__(64 * WN * WM) void k_f8_block(LinearF8Args a, int t
     tile_of(blockIdx.x, tiles_n, tiles_m, tn, tm);
     if (tn >= tiles_n) return;
     const int c0 = tn * BN, m0 = tm * BM;
-    const int blocks = (a.K + kBK - 1) / kBK;
+    const int blocks = (a.K + kBK - 1) / kBK, n = a.K / kBK;   // n: whole ones
     const int8_t *pw = a.w + static_cast<int64_t>(c0) * a.K, *px = a.a + static_cast<int64_t>(m0) * a.K;
     const int8_t *we = a.w + static_cast<int64_t>(a.N) * a.K, *xe = a.a + static_cast<int64_t>(a.M) * a.K;
     const uint32_t nw = span(a.N - c0, a.K), nx = span(a.M - m0, a.K);
-    int off[L], at[L];
+    int off[L], at[kVec ? 1 : L];
 #pragma unroll
     for (int j = 0; j < L; ++j) {
         int row = ((j < LN ? j : j - LN) * NW + wave) * 8 + (lane >> 3);
-        at[j] = 16 * ((lane & 7) ^ swz(row));
-        if (!kVec) row = min(row, j < LN ? a.N - 1 - c0 : a.M - 1 - m0);
-        off[j] = row * a.K + (kVec ? at[j] : 0);
+        const int slot = 16 * ((lane & 7) ^ swz(row));
+        if (!kVec) {
+            row = min(row, j < LN ? a.N - 1 - c0 : a.M - 1 - m0);
+            at[j] = slot;
+        }
+        off[j] = row * a.K + (kVec ? slot : 0);
     }
     // piece j of this wave in a buffer
     auto piece = [&](int j) { return (j < LN ? 0 : BN * kBK) + ((j < LN ? j : j - LN) * NW + wave) * 1024; };
@@ -288,35 +396,19 @@ __global__ __launch_bounds__(64 * WN * WM) void k_f8_block(LinearF8Args a, int t
     // (a tile's last waves may lie past the last channel)
     const float *sw = a.w_scale + static_cast<int64_t>(min(cw, a.N - 1) / kF8Block) * blocks;
     f4 acc[TN][TM] = {};
-    auto read = [&](const int8_t *buf, int b, Codes (&w)[TN], Codes (&x)[TM], float (&s)[TM]) {
-        sc.at(b, sw[b], s);
+    Codes w[TN], x0[TM], x1[TM];
+    float s[TM], sn[TM];
+    auto read_x = [&](const int8_t *buf, Codes (&x)[TM]) {
 #pragma unroll
-        for (int j = 0; j < TM; ++j) {
-            const int8_t *p = buf + (BN + (wm * TM + j) * 16) * kBK;
-            x[j] = Codes{*reinterpret_cast<const i4 *>(p + rd[0]), *reinterpret_cast<const i4 *>(p + rd[1])};
-        }
-#pragma unroll
-        for (int i = 0; i < TN; ++i) {
-            const int8_t *p = buf + (wn * TN + i) * 16 * kBK;
-            w[i] = Codes{*reinterpret_cast<const i4 *>(p + rd[0]), *reinterpret_cast<const i4 *>(p + rd[1])};
-        }
-        if (kVec && (b + 1) * kBK > a.K) {                // zeros past the last k, in both operands
-            const int left = a.K - b * kBK;
-            const bool lo = 16 * g < left, hi = 64 + 16 * g < left;
-            const i4 zero = {0, 0, 0, 0};
-#pragma unroll
-            for (int i = 0; i < TN; ++i) w[i] = Codes{lo ? w[i].lo : zero, hi ? w[i].hi : zero};
-#pragma unroll
-            for (int j = 0; j < TM; ++j) x[j] = Codes{lo ? x[j].lo : zero, hi ? x[j].hi : zero};
-        }
+        for (int j = 0; j < TM; ++j) x[j] = codes_at(buf + (BN + (wm * TM + j) * 16) * kBK, rd);
     };
+    auto read_w = [&](const int8_t *buf, int i) { w[i] = codes_at(buf + (wn * TN + i) * 16 * kBK, rd); };
     i4 v[kVec ? 1 : L];
-    auto load = [&](int b) {                              // past the end: the last block again
-        const int k0 = min(b, blocks - 1) * kBK;
+    auto load = [&](int b) {                              // past the end: the last whole block again
+        if constexpr (!kVec) {
+            const int k0 = min(b, n - 1) * kBK;
 #pragma unroll
-        for (int j = 0; j < L; ++j) {
-            const int8_t *row = (j < LN ? pw : px) + off[j];
-            v[kVec ? 0 : j] = k0 + kBK <= a.K ? any16(row + k0 + at[j]) : load16(row, k0 + at[j], a.K, j < LN ? we : xe);
+            for (int j = 0; j < L; ++j) v[j] = any16((j < LN ? pw : px) + off[j] + k0 + at[j]);
         }
     };
     // block b on its way to its buffer; without 16-byte rows it waits in registers
@@ -331,37 +423,243 @@ __global__ __launch_bounds__(64 * WN * WM) void k_f8_block(LinearF8Args a, int t
             load(b + 1);
         }
     };
-    Codes w0[TN], x0[TM], w1[TN], x1[TM];
-    float s0[TM], s1[TM];
-    if (!kVec) load(0);
+    // block b is in cur and, read, in w and x; the next one goes to w and y
+    auto step = [&](int8_t *cur, const int8_t *nxt, int b, const Codes (&x)[TM], Codes (&y)[TM]) {
 #pragma unroll
-    for (int i = 0; i < S; ++i) fetch(ring[i], i);
+        for (int j = 0; j < TM; ++j) s[j] = sn[j];
+        wait_mem<kVec ? (S - 2) * L : 0, true>();         // block b + 1 has landed, cur is read
+        barrier();
+        const int next = min(b + 1, blocks - 1);
+        sc.at(next, sw[next], sn);
+        fetch(cur, b + S);
+        read_x(nxt, y);
+        mul_block<kWide>(w, x, s, acc, [&](int i) { read_w(nxt, i); });
+        __builtin_amdgcn_sched_barrier(0);                // registers do not live over two steps
+    };
+    sc.at(0, sw[0], sn);
+    if (kVec || n > 0) {
+        load(0);
+        fetch(r0, 0);
+        fetch(r1, 1);
+        if constexpr (S > 2) {
+            fetch(r2, 2);
+            fetch(r3, 3);
+        }
+    }
+    if (n > 0) {
+        wait_mem<0, true>();
+        barrier();
+        read_x(r0, x0);
+#pragma unroll
+        for (int i = 0; i < TN; ++i) read_w(r0, i);
+        // whole rounds of the ring, then what is left, as in k_f8_ring
+        int b = 0;
+        for (; b + S <= n; b += S) {
+            step(r0, r1, b, x0, x1);
+            if constexpr (S > 2) {
+                step(r1, r2, b + 1, x1, x0);
+                step(r2, r3, b + 2, x0, x1);
+                step(r3, r0, b + 3, x1, x0);
+            } else {
+                step(r1, r0, b + 1, x1, x0);
+            }
+        }
+        if (b < n) {
+            step(r0, r1, b, x0, x1);
+            if constexpr (S > 2)
+                if (b + 1 < n) {
+                    step(r1, r2, b + 1, x1, x0);
+                    if (b + 2 < n) step(r2, r3, b + 2, x0, x1);
+                }
+        }
+    }
+    // the last fetches have landed, and every wave is done with the ring
+    wait_mem<0, true>();
+    __syncthreads();
+    if (n < blocks) {                                     // the block past the whole ones
+        const int slot = kVec ? n % S : 0;
+        int8_t *buf = slot == 0 ? r0 : slot == 1 ? r1 : slot == 2 ? r2 : r3;
+        if constexpr (!kVec) {
+#pragma unroll
+            for (int j = 0; j < L; ++j)
+                *reinterpret_cast<i4 *>(buf + piece(j) + lane * 16) =
+                    load16((j < LN ? pw : px) + off[j], n * kBK + at[j], a.K, j < LN ? we : xe);
+            __syncthreads();
+        }
+        read_x(buf, x0);
+#pragma unroll
+        for (int i = 0; i < TN; ++i) read_w(buf, i);
+        if (kVec) clear_past(a.K - n * kBK, g, w, x0);
+        mul_block<kWide>(w, x0, sn, acc, [](int) {});
+        __syncthreads();
+    }
+    write_tile<OT, TN, TM>(a, cw, mw, lane, r0 + wave * kStageBytes, acc);
+}
+
+// -------------------------------------------------------------- large product
+// Persistent workgroups over tiles of 256 channels x 256 tokens, 8 waves of 64 x
+// 128 each: 128 accumulators a lane, two waves a SIMD, all of LDS (two buffers of
+// one block, and the waves' pieces for the stores).  k is a multiple of 256, the
+// outputs have 16 bits.  A block's token tiles go through two at a time, the next
+// two on their way from LDS meanwhile; during the last two, the block's
+// weights give way to the next block's one by one, behind the barrier that
+// hands the buffer back to the fetches.  The fetches run two blocks ahead and over
+// tile borders.
+template <typename OT>
+__global__ __launch_bounds__(512) void k_f8_tile(LinearF8Args a, int tiles_n, int tiles_m) {
+    constexpr int BN = 256, BM = 256, WN = 4, NW = 8;
+    constexpr int TN = BN / WN / 16, TM = BM / (NW / WN) / 16;
+    constexpr int F = BN / 8 / NW;                        // fetches of an operand's block a wave makes
+    __shared__ alignas(1024) int8_t b0[(BN + BM) * kBK], b1[(BN + BM) * kBK];
+    constexpr int kStage = 16 * TN * 16 * sizeof(typename OT::bits);
+    __shared__ alignas(16) int8_t stage[NW * kStage];
+    __shared__ float sl[2][BM];                           // a block's token scales, and the next one's
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, g = lane >> 4;
+    const int wn = wave % WN, wm = wave / WN;
+    const int blocks = a.K / kBK;                         // of a tile, in pairs
+    const int all = tiles_n * tiles_m;
+
+    // each XCD (ids modulo 8) takes a run of consecutive tiles
+    const int per_xcd = (all + 7) / 8, stride = gridDim.x / 8;
+    const int first = (blockIdx.x & 7) * per_xcd, end = min(all, first + per_xcd);
+    int tile = first + (blockIdx.x >> 3);
+    if (tile >= end) return;
+
+    int off[F];
+#pragma unroll
+    for (int j = 0; j < F; ++j) {
+        const int row = (j * NW + wave) * 8 + (lane >> 3);
+        off[j] = row * a.K + 16 * ((lane & 7) ^ swz(row));
+    }
+    const int rd[2] = {r * kBK + 16 * (g ^ swz(r)), r * kBK + 16 * ((4 + g) ^ swz(r))};
+
+    // The fetch stream: block fb of tile ft, and the tile after it (past the last
+    // tile, that one again).
+    Tile t = tile_at(tile, tiles_n, tiles_m);
+    int fb = 0, ft = tile, ftn = tile;
+    const int8_t *pw = a.w + static_cast<int64_t>(t.n) * BN * a.K, *pwn = pw;
+    const int8_t *px = a.a + static_cast<int64_t>(t.m) * BM * a.K, *pxn = px;
+    uint32_t nw = span(a.N - t.n * BN, a.K), nwn = nw, nx = span(a.M - t.m * BM, a.K), nxn = nx;
+    auto aim = [&]() {
+        ftn = ft + stride < end ? ft + stride : ft;
+        const Tile f = tile_at(ftn, tiles_n, tiles_m);
+        pwn = a.w + static_cast<int64_t>(f.n) * BN * a.K;
+        pxn = a.a + static_cast<int64_t>(f.m) * BM * a.K;
+        nwn = span(a.N - f.n * BN, a.K);
+        nxn = span(a.M - f.m * BM, a.K);
+    };
+    auto fetch = [&](int8_t *buf) {
+        const int k0 = fb * kBK;
+#pragma unroll
+        for (int j = 0; j < F; ++j) fetch16(buf + (j * NW + wave) * 1024, pw, nw, off[j], k0);
+#pragma unroll
+        for (int j = 0; j < F; ++j) fetch16(buf + BN * kBK + (j * NW + wave) * 1024, px, nx, off[j], k0);
+        const bool wrap = ++fb == blocks;                  // at most once a tile
+        fb = wrap ? 0 : fb;
+        ft = wrap ? ftn : ft;
+        pw = wrap ? pwn : pw;
+        px = wrap ? pxn : px;
+        nw = wrap ? nwn : nw;
+        nx = wrap ? nxn : nx;
+    };
+    f4 acc[TN][TM];
+    Codes w[TN], x[2][2];
+    float s[2][2], sb = 0.0f;                             // scales of two token tiles, and of the channels
+    int32_t so = 0;                                       // the row of a_scale that this thread fetches
+    const int token = threadIdx.x % BM;
+    const float *sw = nullptr;
+    auto read_s = [&](int buf, int jp) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) s[jp & 1][j] = sl[buf][(wm * TM + 2 * jp + j) * 16 + r];
+    };
+    auto read_x = [&](const int8_t *buf, int jp) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) x[jp & 1][j] = codes_at(buf + (BN + (wm * TM + 2 * jp + j) * 16) * kBK, rd);
+    };
+    auto read_w = [&](const int8_t *buf, int i) { w[i] = codes_at(buf + (wn * TN + i) * 16 * kBK, rd); };
+    // The token tiles 2 jp and 2 jp + 1 against all channels; two sums are on their way
+    // while one joins.  In the last pair the weights give way to those in next.
+    auto pair = [&](int jp, const int8_t *next, auto last) {
+        const float s0 = s[jp & 1][0] * sb, s1 = s[jp & 1][1] * sb;
+        f4 p[2];
+#pragma unroll
+        for (int t = 0; t < 2 * TN + 2; ++t) {
+            f4 q = {};
+            if (t < 2 * TN) q = mul(w[t / 2], x[jp & 1][t % 2]);
+            in_order();
+            if (t > 1) join(acc[t / 2 - 1][2 * jp + t % 2], p[t % 2], t % 2 ? s1 : s0);
+            in_order();
+            p[t % 2] = q;
+            if (decltype(last)::value && t % 2 == 1 && t < 2 * TN) read_w(next, t / 2);
+        }
+    };
+    // Block b of the tile is in cur, its weights, first token tiles and their scales in
+    // registers, the next block (of this tile or the next) on its way to nxt.  Before
+    // the last two token tiles everything on its way has landed, cur goes back to the
+    // fetches and the next block's first operands are read.  (All that is waited for
+    // is waited for there: a scale that is loaded later would wait for the fetches
+    // too.)  parity: which of sl block b has.
+    auto block = [&](int8_t *cur, int8_t *nxt, int b, int parity) {
+        const int next = min(b + 1, blocks - 1);          // (a tile's last block: its own again, unused)
+        const float sa = a.a_scale[so + next], sbn = sw[next];
+#pragma unroll
+        for (int jp = 0; jp + 1 < TM / 2; ++jp) {
+            read_x(cur, jp + 1);
+            read_s(parity, jp + 1);
+            pair(jp, cur, std::false_type{});
+        }
+        wait_mem<0, true>();
+        sl[parity ^ 1][token] = sa;                       // two threads a token write the same
+        wait_mem<0, true>();
+        barrier();
+        fetch(cur);
+        read_x(nxt, 0);
+        read_s(parity ^ 1, 0);
+        pair(TM / 2 - 1, nxt, std::true_type{});
+        sb = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, sbn)));
+    };
+    // A tile's scales: those of its first block go to sl[0].
+    auto enter = [&]() {
+        sw = a.w_scale + static_cast<int64_t>(min(t.n * BN + wn * TN * 16, a.N - 1) / kF8Block) * blocks;
+        so = min(t.m * BM + token, a.M - 1) * blocks;
+        sl[0][token] = a.a_scale[so];
+        sb = sw[0];
+    };
+    aim();
+    fetch(b0);
+    fetch(b1);
+    enter();
     wait_mem<0, true>();
     barrier();
-    read(ring[0], 0, w0, x0, s0);
-    int slot = 0;
-    for (int b = 0; b < blocks; b += 2) {
-        int next = slot + 1 == S ? 0 : slot + 1;
-        wait_mem<kVec ? (S - 2) * L : 0, true>();         // block b + 1 has landed, block b is read
-        barrier();
-        if (b + 1 < blocks) read(ring[next], b + 1, w1, x1, s1);
-        fetch(ring[slot], b + S);
-        mul_block<kWide>(w0, x0, s0, acc);
-        if (b + 1 >= blocks) break;
-        slot = next;
-        next = slot + 1 == S ? 0 : slot + 1;
-        wait_mem<kVec ? (S - 2) * L : 0, true>();
-        barrier();
-        if (b + 2 < blocks) read(ring[next], b + 2, w0, x0, s0);
-        fetch(ring[slot], b + 1 + S);
-        mul_block<kWide>(w1, x1, s1, acc);
-        slot = next;
+    read_x(b0, 0);
+#pragma unroll
+    for (int i = 0; i < TN; ++i) read_w(b0, i);
+    for (;;) {
+        read_s(0, 0);
+        aim();
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+            for (int j = 0; j < TM; ++j) acc[i][j] = f4{0, 0, 0, 0};
+        for (int b = 0; b < blocks; b += 2) {
+            block(b0, b1, b, 0);
+            block(b1, b0, b + 1, 1);
+        }
+        const Tile done = t;
+        tile += stride;
+        if (tile < end) {
+            // the last block's scales are in sl[1] and every wave is past those of sl[0]
+            t = tile_at(tile, tiles_n, tiles_m);
+            enter();
+        }
+        write_tile<OT, TN, TM>(a, done.n * BN + wn * TN * 16, done.m * BM + wm * TM * 16, lane, stage + wave * kStage, acc);
+        if (tile >= end) break;
+        wait_mem<63, true>();
+        barrier();                                        // sl[0] is written
     }
     wait_mem<0, true>();                                  // nothing lands in LDS after the end
-#pragma unroll
-    for (int i = 0; i < TN; ++i)
-#pragma unroll
-        for (int j = 0; j < TM; ++j) put4<OT>(a, cw + 16 * i + 4 * g, mw + 16 * j + r, acc[i][j]);
 }
 
 // ------------------------------------------------------------------- dispatch
@@ -389,13 +687,24 @@ hipError_t launch_block(const LinearF8Args &a, hipStream_t s) {
 }
 
 template <typename OT>
+hipError_t launch_tile(const LinearF8Args &a, int cus, hipStream_t s) {
+    const int tn = static_cast<int>(tiles(a.N, 256)), tm = static_cast<int>(tiles(a.M, 256));
+    const int64_t all = static_cast<int64_t>(tn) * tm, most = cus >= 8 ? cus / 8 * 8 : 8;
+    const dim3 grid(static_cast<unsigned>(all < most ? (all + 7) / 8 * 8 : most));
+    k_f8_tile<OT><<<grid, dim3(512), 0, s>>>(a, tn, tm);
+    return hipGetLastError();
+}
+
+template <typename OT>
 hipError_t launch(const LinearF8Args &a, hipStream_t s) {
     const int cus = device_cus();
     const auto fits = [&](int bn, int bm) {
         return (bn <= 64 || bn < 2 * a.N) && (bm <= 16 || bm < 2 * a.M) &&
                2 * tiles(a.N, bn) * tiles(a.M, bm) > static_cast<int64_t>(cus);
     };
-    if (fits(256, 128)) return launch_block<OT, 256, 128, 4, 2, 3>(a, s);
+    if constexpr (!__is_same(OT, F32))
+        if (fits(256, 256) && a.K % 256 == 0 && static_cast<int64_t>(a.M) * (a.K / kBK) < INT32_MAX)
+            return launch_tile<OT>(a, cus, s);
     if (fits(128, 128)) return launch_block<OT, 128, 128, 2, 4, 4>(a, s);
     if (fits(64, 128)) return launch_block<OT, 64, 128, 2, 2, 4>(a, s);
     if (fits(64, 64)) return launch_ring<OT, 4, 4, 4, 2>(a, s);

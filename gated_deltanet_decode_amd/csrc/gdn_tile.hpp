@@ -106,5 +106,19 @@ inline dim3 tile_grid(int64_t tiles_n, int64_t tiles_m) {
 
 constexpr int64_t tiles(int64_t n, int64_t b) { return (n + b - 1) / b; }
 
+struct Tile {
+    int n, m;
+};
+// Tile i in an order that keeps neighbours close: groups of 8 token tiles by
+// all channel tiles.
+__device__ __forceinline__ Tile tile_at(int i, int tiles_n, int tiles_m) {
+    constexpr int kG = 8;
+    const int per = kG * tiles_n;
+    const int grp = i / per, in = i - grp * per;
+    const int gm = min(kG, tiles_m - grp * kG);
+    const int n = in / gm;
+    return Tile{__builtin_amdgcn_readfirstlane(n), __builtin_amdgcn_readfirstlane(grp * kG + in - n * gm)};
+}
+
 }  // namespace
 }  // namespace gdn
