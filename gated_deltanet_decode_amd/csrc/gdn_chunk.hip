@@ -15,9 +15,7 @@ hipError_t launch(const ChunkArgs &a, hipStream_t s) {
     p.k = a.k;
     p.beta = a.beta;
     p.gate = a.gate;
-    p.T = a.T;
-    p.P = a.P;
-    p.vec = a.vec;
+    p.within = a.within;
     p.kq = a.kq;
     const hipError_t e = launch_prep<ET, NP, NO, false>(p, s);
     if (e != hipSuccess) return e;

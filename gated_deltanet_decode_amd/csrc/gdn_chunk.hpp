@@ -36,18 +36,19 @@ constexpr int64_t chunk_places(int64_t B, int64_t tokens) { return tokens / kChu
 constexpr int planes_in(int type) { return type == 0 ? 3 : type == 1 ? 1 : 2; }
 constexpr int planes_out(int type) { return type == 0 ? 3 : 2; }
 
-// What a chunk's tokens do to each other, per chunk place and value head:
-//   T  (I + A)^-1, its ten lower blocks of 16 x 16 floats, each in the order in
-//      which the lanes of a wave read it as an operand;
-//   P  the masked, decayed and scaled Q K^T in planes_out bf16 planes: six
-//      operands of 16 tokens x 32 tokens each;
-//   vec rise, fall and beta of the 64 tokens;
-// and, unless the inputs are bf16, the planes of k and q per chunk place and key
-// head, as LDS holds them.
+// What a chunk's tokens do to each other, a block per chunk place and value head, as
+// LDS holds it:
+//   T    (I + A)^-1, its ten lower blocks of 16 x 16 floats, each in the order in
+//        which the lanes of a wave read it as an operand;
+//   P    the masked, decayed and scaled Q K^T in bf16 planes: six operands of 16
+//        tokens x 32 tokens each;
+//   vec  rise, fall and beta of the 64 tokens.
+// And, unless the inputs are bf16, the planes of k and q per chunk place and key
+// head.
 constexpr int kTBlocks = 10, kPBlocks = 6;
 constexpr int kTBytes = kTBlocks * 1024;
 constexpr int kVecFloats = 3 * kChunk;
-constexpr size_t p_bytes(int type) { return static_cast<size_t>(kPBlocks) * 1024 * planes_out(type); }
+constexpr int within_bytes(int planes) { return kTBytes + kPBlocks * 1024 * planes + 1024; }
 
 struct ChunkArgs {
     Packed s;
@@ -60,9 +61,7 @@ struct ChunkArgs {
     float *state_out;                // NULL: not wanted
     void *out;
     // workspace
-    float *T;
-    char *P;
-    float *vec;
+    char *within;                    // T, P and vec
     char *kq;                        // NULL for bf16
     // the backward pass alone
     const void *d_out;
@@ -83,8 +82,7 @@ struct BackArgs {
     float *dbeta;
     float *dgate;
     // workspace
-    float *Tn;                       // T's blocks, read along their columns
-    char *Pn;                        // P's operands transposed, three planes
+    char *back;                      // as within: T read along its columns, P transposed, vec
     double *gsum;                    // [place][Hv][64] running sums of the gates
     float *dstates;                  // [place][Hv][dv][dk] that leave the chunks
     float *r;                        // [place][Hv][64][dv]

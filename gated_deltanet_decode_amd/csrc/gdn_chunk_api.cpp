@@ -72,20 +72,16 @@ bool sizes_ok(const gdn_dims *d, int32_t B, int32_t tokens, int32_t type) {
 
 // Where the parts of the workspace begin, each a multiple of 16 bytes.
 struct ChunkSpace {
-    size_t T, P, vec, kq, bytes;
+    size_t kq, bytes;                // the blocks first
     ChunkSpace(const gdn_dims *d, int32_t B, int32_t tokens, int32_t type) {
         const size_t places = static_cast<size_t>(gdn::chunk_places(B, tokens));
         const size_t pv = places * d->n_v_heads, pk = places * d->n_k_heads;
-        T = 0;
-        P = T + pv * gdn::kTBytes;
-        vec = P + pv * gdn::p_bytes(type);
-        kq = vec + pv * gdn::kVecFloats * sizeof(float);
+        kq = pv * gdn::within_bytes(gdn::planes_out(type));
         bytes = kq + (type == GDN_BF16 ? 0 : pk * 2 * gdn::planes_in(type) * gdn::kPlaneBytes);
     }
 };
-
 struct BackSpace {
-    size_t T, P, vec, kq, Tn, Pn, gsum, states, dstates, delta, r, od, du, bytes;
+    size_t kq, within, back, gsum, states, dstates, delta, r, od, du, bytes;
     BackSpace(const gdn_dims *d, int32_t B, int32_t tokens, int32_t type) {
         const size_t places = static_cast<size_t>(gdn::chunk_places(B, tokens));
         const size_t pv = places * d->n_v_heads, pk = places * d->n_k_heads;
@@ -97,11 +93,8 @@ struct BackSpace {
         dstates = take(pv * D * D * f);
         delta = take(pv * C * D * f);
         r = take(pv * C * D * f);
-        T = take(pv * gdn::kTBytes);
-        Tn = take(pv * gdn::kTBytes);
-        P = take(pv * gdn::p_bytes(GDN_F32));
-        Pn = take(pv * gdn::p_bytes(GDN_F32));
-        vec = take(pv * gdn::kVecFloats * f);
+        within = take(pv * gdn::within_bytes(3));
+        back = take(pv * gdn::within_bytes(3));
         od = take(pv * 8 * C * f);
         du = take(pv * 8 * f);
         kq = take(type == GDN_BF16 ? 0 : pk * 2 * gdn::planes_in(type) * gdn::kPlaneBytes);
@@ -184,9 +177,7 @@ int gdn_chunk(const gdn_dims *dims, int32_t B, int32_t tokens, int32_t type, con
     a.state_out = state_out;
     a.out = out;
     char *p = static_cast<char *>(workspace);
-    a.T = reinterpret_cast<float *>(p + w.T);
-    a.P = p + w.P;
-    a.vec = reinterpret_cast<float *>(p + w.vec);
+    a.within = p;
     a.kq = type == GDN_BF16 ? nullptr : p + w.kq;
     (void)hipGetLastError();
     return hip_status(gdn::launch_chunk(a, static_cast<hipStream_t>(stream)), "gdn_chunk launch");
@@ -241,9 +232,7 @@ int gdn_chunk_backward(const gdn_dims *dims, int32_t B, int32_t tokens, int32_t 
     a.f.gate = gate;
     a.f.state = state;
     a.f.d_out = d_out;
-    a.f.T = at(w.T);
-    a.f.P = p + w.P;
-    a.f.vec = at(w.vec);
+    a.f.within = p + w.within;
     a.f.kq = type == GDN_BF16 ? nullptr : p + w.kq;
     a.f.states = at(w.states);
     a.f.delta = at(w.delta);
@@ -255,8 +244,7 @@ int gdn_chunk_backward(const gdn_dims *dims, int32_t B, int32_t tokens, int32_t 
     a.dv = dv;
     a.dbeta = dbeta;
     a.dgate = dgate;
-    a.Tn = at(w.Tn);
-    a.Pn = p + w.Pn;
+    a.back = p + w.back;
     a.gsum = reinterpret_cast<double *>(p + w.gsum);
     a.dstates = at(w.dstates);
     a.r = at(w.r);

@@ -22,12 +22,6 @@
 namespace gdn {
 namespace {
 
-template <int NP>
-struct BackStage {
-    static constexpr int kK = 0, kQ = NP * kPlaneBytes, kT = 2 * NP * kPlaneBytes, kP = kT + kTBytes,
-                         kVec = kP + kPBlocks * 1024 * 3, kBytes = kVec + 1024;
-};
-
 // Two of a token's planes as an operand: elements of tokens 4 g + e of tiles a and b.
 template <typename ET, int NP>
 __device__ __forceinline__ void planes_in(const typename ET::bits *x, u4 (&p)[NP]) {
@@ -82,7 +76,7 @@ __device__ __forceinline__ void load_kq(const ChunkArgs &a, char *to, int place,
 template <typename ET, int NP, int W, int S>
 __global__ __launch_bounds__(64 * W) void k_back(BackArgs a, int parts) {
     typedef typename ET::bits bits;
-    typedef BackStage<NP> L;
+    typedef Stage<NP, 3> L;
     __shared__ alignas(1024) char buf0[L::kBytes], buf1[S > 1 ? L::kBytes : 16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
@@ -105,31 +99,19 @@ __global__ __launch_bounds__(64 * W) void k_back(BackArgs a, int parts) {
                              : f4{0, 0, 0, 0};
     const int place0 = place_of(sp.first, b);
     auto fetch = [&](char *to, int c) {
-        const int64_t place = place0 + c, ph = place * Hv + h;
+        const int64_t place = place0 + c;
         const int rows = min(kChunk, sp.len - c * kChunk);
-        fetch_rows<ET, NP, W>(a.f, to, to + L::kQ, place, sp.first + c * kChunk, rows, kh, wave, lane);
-        const float *T = a.Tn + ph * (kTBlocks * 256);
-        const char *P = a.Pn + ph * (kPBlocks * 1024 * 3);
-        for (int i = wave; i < kTBlocks + kPBlocks * 3 + 1; i += W) {
-            if (i < kTBlocks)
-                fetch16(to + L::kT + i * 1024, T, kTBytes, lane * 16, i * 1024);
-            else if (i < kTBlocks + kPBlocks * 3)
-                fetch16(to + L::kP + (i - kTBlocks) * 1024, P, kPBlocks * 1024 * 3, lane * 16, (i - kTBlocks) * 1024);
-            else
-                fetch16(to + L::kVec, a.f.vec + ph * kVecFloats, kVecFloats * 4, lane * 16, 0);
-        }
+        fetch_rows<ET, NP, W>(a.f, to + L::kK, to + L::kQ, place, sp.first + c * kChunk, rows, kh, wave, lane);
+        fetch_block<within_bytes(3), W>(a.back + (place * Hv + h) * within_bytes(3), to + L::kT, wave, lane);
     };
-    const int64_t vstride = static_cast<int64_t>(Hv) * kHeadDim;
-    const int64_t vat = (static_cast<int64_t>(sp.first) * Hv + h) * kHeadDim + dv;
-    const bits *dop = static_cast<const bits *>(a.f.d_out) + vat;
-    bits *dvp = static_cast<bits *>(a.dv) + vat;
+    auto rows_of = [&](const void *base, int c) {
+        return Rows<ET>(base, static_cast<int64_t>(sp.first) + c * kChunk, min(kChunk, sp.len - c * kChunk), h, Hv);
+    };
     bits on[16];                                          // d_out of the chunk to come
     auto load_o = [&](int c) {
+        const Rows<ET> o = rows_of(a.f.d_out, c);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int t = c * kChunk + 16 * (i / 4) + 4 * g + i % 4;
-            on[i] = t < sp.len ? dop[t * vstride] : bits(0);
-        }
+        for (int i = 0; i < 16; ++i) on[i] = o.load(16 * (i / 4) + 4 * g + i % 4, dv);
     };
 
     auto chunk = [&](char *cur, char *nxt, int c) {
@@ -144,8 +126,12 @@ __global__ __launch_bounds__(64 * W) void k_back(BackArgs a, int parts) {
         if (S == 1) {
             meet();
             fetch(cur, c);
+            wait_all<0>();
+        } else {
+            // This chunk's fetches have landed; behind them came 32 stores of R and dV, 16
+            // loads of d_out, 8 stores of G and 16 loads of Delta.
+            wait_all<48>();
         }
-        wait_all<0>();
         const int rows = min(kChunk, sp.len - c * kChunk);
         clear_rows<NP, W>(cur, cur + L::kQ, rows);
         meet();
@@ -191,6 +177,7 @@ __global__ __launch_bounds__(64 * W) void k_back(BackArgs a, int parts) {
         for (int d = 1; d < 64; d *= 2) du += __shfl_xor(du, d);
         if (lane == 0) a.du[ph * 8 + part * W + wave] = du;
         f4 R[4];
+        const Rows<ET> dvr = rows_of(a.dv, c);
 #pragma unroll
         for (int jt = 0; jt < 4; ++jt) {
             R[jt] = f4{0, 0, 0, 0};
@@ -204,8 +191,7 @@ __global__ __launch_bounds__(64 * W) void k_back(BackArgs a, int parts) {
             for (int e = 0; e < 4; ++e) {
                 to[e * kHeadDim] = R[jt][e];
                 R[jt][e] *= fabsf(beta[e]) <= kLeastBeta ? 0.0f : beta[e];
-                const int t = c * kChunk + 16 * jt + 4 * g + e;
-                if (t < sp.len) dvp[t * vstride] = ET::put(R[jt][e]);
+                dvr.store(16 * jt + 4 * g + e, dv, R[jt][e]);
             }
         }
         // the gradient of the state that enters the chunk
@@ -242,8 +228,9 @@ __global__ __launch_bounds__(64 * W) void k_back(BackArgs a, int parts) {
         if (c > 0) load_o(c - 1);
     };
     if (chunks > 0) {
-        load_o(chunks - 1);
         if (S > 1) fetch(buf0, chunks - 1);
+        load_o(chunks - 1);
+        wait_all<0>();
         int c = chunks - 1;
         if constexpr (S > 1) {
             for (; c >= 1; c -= 2) {
@@ -303,7 +290,8 @@ __global__ __launch_bounds__(256) void k_grad(BackArgs a) {
         const int64_t ph = static_cast<int64_t>(place) * Hv + h;
         if (x > 0) __syncthreads();                       // the last head is done with LDS
         if (threadIdx.x < kChunk) gs[threadIdx.x] = a.gsum[ph * kChunk + threadIdx.x];
-        if (threadIdx.x < kVecFloats) vec[threadIdx.x] = a.f.vec[ph * kVecFloats + threadIdx.x];
+        if (threadIdx.x < kVecFloats) vec[threadIdx.x] = reinterpret_cast<const float *>(
+            a.f.within + (ph + 1) * within_bytes(3) - 1024)[threadIdx.x];
         f4 Z[8] = {}, Wm[8] = {}, H[8] = {};
         // lane: own token; elements: the other's.  F1, E1 of tiles up to the own, F2, E2
         // from it on.
@@ -496,6 +484,24 @@ __global__ __launch_bounds__(256) void k_grad(BackArgs a) {
     }
 }
 
+// Waves a workgroup as in launch_walk.
+template <typename ET, int NP, int W, int S>
+hipError_t launch_back_of(const BackArgs &a, hipStream_t s) {
+    const int parts = 8 / W;
+    const int64_t wgs = static_cast<int64_t>(a.f.s.B) * a.f.s.Hv * parts;
+    k_back<ET, NP, W, S><<<dim3(static_cast<unsigned>((wgs + 7) / 8 * 8)), dim3(64 * W), 0, s>>>(a, parts);
+    return hipGetLastError();
+}
+template <typename ET, int NP, int S>
+hipError_t launch_back(const BackArgs &a, hipStream_t s) {
+    const int64_t heads = static_cast<int64_t>(a.f.s.B) * a.f.s.Hv;
+    const int cus = device_cus();
+    if (heads * 8 <= cus) return launch_back_of<ET, NP, 1, S>(a, s);
+    if (heads * 4 <= cus) return launch_back_of<ET, NP, 2, S>(a, s);
+    if (heads * 2 <= cus) return launch_back_of<ET, NP, 4, S>(a, s);
+    return launch_back_of<ET, NP, 8, S>(a, s);
+}
+
 template <typename ET, int NP, int NO, int S>
 hipError_t launch(const BackArgs &a, hipStream_t s) {
     PrepArgs p{};
@@ -504,21 +510,15 @@ hipError_t launch(const BackArgs &a, hipStream_t s) {
     p.k = a.f.k;
     p.beta = a.f.beta;
     p.gate = a.f.gate;
-    p.T = a.f.T;
-    p.P = a.f.P;
-    p.vec = a.f.vec;
+    p.within = a.f.within;
     p.kq = a.f.kq;
-    p.Tn = a.Tn;
-    p.Pn = a.Pn;
+    p.back = a.back;
     p.gsum = a.gsum;
     hipError_t e = launch_prep<ET, NP, 3, true>(p, s);
     if (e != hipSuccess) return e;
     e = launch_walk<ET, NP, 3, S, true>(a.f, s);
     if (e != hipSuccess) return e;
-    constexpr int W = 8;
-    const int64_t wgs = static_cast<int64_t>(a.f.s.B) * a.f.s.Hv * (8 / W);
-    k_back<ET, NP, W, S><<<dim3(static_cast<unsigned>((wgs + 7) / 8 * 8)), dim3(64 * W), 0, s>>>(a, 8 / W);
-    e = hipGetLastError();
+    e = launch_back<ET, NP, S>(a, s);
     if (e != hipSuccess) return e;
     const int64_t places = chunk_places(a.f.s.B, a.f.s.tokens) * a.f.s.Hk;
     k_grad<ET, NP, NO><<<dim3(static_cast<unsigned>(places)), dim3(256), 0, s>>>(a);

@@ -53,6 +53,21 @@ __device__ __forceinline__ f4 mma_planes(const u4 (&a)[NA], const u4 (&b)[NB], f
     return c;
 }
 
+// The same for N operands against one, plane by plane, so that neighbouring
+// instructions do not wait for each other; kFirst: the N come first.
+template <int L, bool kFirst, int N, int NA, int NB>
+__device__ __forceinline__ void mma_planes(const u4 (&a)[N][NA], const u4 (&b)[NB], f4 (&c)[N]) {
+#pragma unroll
+    for (int t = L; t >= 0; --t)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+                if (i + j == t)
+#pragma unroll
+                    for (int n = 0; n < N; ++n) c[n] = kFirst ? mma(a[n][i], b[j], c[n]) : mma(b[j], a[n][i], c[n]);
+}
+
 // The upper halves of two words, as two bf16 (truncated floats).
 __device__ __forceinline__ uint32_t upper(uint32_t lo, uint32_t hi) {
     return __builtin_amdgcn_perm(hi, lo, 0x07060302);
@@ -98,6 +113,53 @@ __device__ __forceinline__ void meet() {
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
+
+// Rows of a head's tokens in a [tokens][heads][128] tensor, those of one chunk: an
+// access past the last row reads zero and writes nothing.
+template <typename ET>
+struct Rows {
+    typedef typename ET::bits bits;
+    static constexpr int kBytes = sizeof(bits);
+    __amdgpu_buffer_rsrc_t rows;
+    int stride;                                           // bytes from token to token
+    // `first` tokens into the tensor, n of them, head h of H
+    __device__ __forceinline__ Rows(const void *base, int64_t first, int n, int h, int H) {
+        stride = H * 128 * kBytes;
+        rows = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<char *>(static_cast<const char *>(base)) + (first * H + h) * (128 * kBytes), 0,
+            static_cast<uint32_t>(n - 1) * stride + 128 * kBytes, 0x00020000);
+    }
+    __device__ __forceinline__ bits load(int token, int at) const {
+        if constexpr (kBytes == 2)
+            return __builtin_bit_cast(bits, __builtin_amdgcn_raw_buffer_load_b16(rows, token * stride + at * kBytes, 0, 0));
+        else
+            return __builtin_bit_cast(bits, __builtin_amdgcn_raw_buffer_load_b32(rows, token * stride + at * kBytes, 0, 0));
+    }
+    __device__ __forceinline__ f4 load4(int token, int at) const {
+        if constexpr (kBytes == 2) {
+            typedef bits b4 __attribute__((ext_vector_type(4)));
+            const b4 v = __builtin_bit_cast(b4, __builtin_amdgcn_raw_buffer_load_b64(rows, token * stride + at * kBytes, 0, 0));
+            return f4{ET::get(v[0]), ET::get(v[1]), ET::get(v[2]), ET::get(v[3])};
+        } else {
+            return __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(rows, token * stride + at * kBytes, 0, 0));
+        }
+    }
+    __device__ __forceinline__ void store(int token, int at, float x) const {
+        if constexpr (kBytes == 2)
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, ET::put(x)), rows, token * stride + at * kBytes, 0, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, x), rows, token * stride + at * kBytes, 0, 0);
+    }
+    __device__ __forceinline__ void store4(int token, int at, f4 x) const {
+        if constexpr (kBytes == 2) {
+            typedef bits b4 __attribute__((ext_vector_type(4)));
+            const b4 v = {ET::put(x[0]), ET::put(x[1]), ET::put(x[2]), ET::put(x[3])};
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u2, v), rows, token * stride + at * kBytes, 0, 0);
+        } else {
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, x), rows, token * stride + at * kBytes, 0, 0);
+        }
+    }
+};
 
 }  // namespace
 }  // namespace gdn

@@ -29,19 +29,18 @@ struct PrepArgs {
     const void *k;
     const float *beta;
     const float *gate;
-    float *T;                        // blocks read along their rows
-    char *P;
-    float *vec;
+    char *within;                    // a block per chunk place and value head
     char *kq;
     // the backward pass alone
-    float *Tn;                       // and along their columns
-    char *Pn;
+    char *back;                      // the same with T and P transposed
     double *gsum;
 };
 
-// A row of a plane is 16 chunks of 16 bytes; chunk c of row r lies at slot
-// c ^ (r & 15), which spreads the rows that an instruction reads over all banks.
-__device__ __forceinline__ int plane_at(int row, int chunk) { return row * 256 + ((chunk ^ (row & 15)) << 4); }
+// A row of a plane is 16 chunks of 16 bytes; chunk c of row r lies at slot c ^ turn(r).
+// Sixteen rows at a chunk and four neighbouring rows at four neighbouring chunks
+// (read_columns) both spread over all banks.
+__device__ __forceinline__ int turn(int row) { return (row & 3) << 2 | (row >> 2 & 3); }
+__device__ __forceinline__ int plane_at(int row, int chunk) { return row * 256 + ((chunk ^ turn(row)) << 4); }
 
 constexpr int block_of(int it, int jt) { return it * (it + 1) / 2 + jt; }
 // Operand of 16 tokens it x 32 tokens of half h.
@@ -88,6 +87,7 @@ __device__ __forceinline__ float beta_of(float x) {
 template <typename ET, int NP, int NO, bool kBack>
 __global__ __launch_bounds__(256) void k_prep(PrepArgs a) {
     constexpr int HB = 2;
+    constexpr int kBlock = within_bytes(NO), kBackBlock = within_bytes(3);
     __shared__ alignas(16) char kp[NP][kPlaneBytes], qp[NP][kPlaneBytes];
     __shared__ alignas(16) float As[HB][kTBlocks][256], Td[HB][4][256];
     __shared__ double gs[HB][kChunk];
@@ -167,11 +167,18 @@ __global__ __launch_bounds__(256) void k_prep(PrepArgs a) {
             gs[wave][lane] = x;
             bs[wave][lane] = beta;
             const double last = lane_of(x, 63);
-            float *vec = a.vec + (static_cast<int64_t>(place) * a.s.Hv + h) * kVecFloats;
-            vec[lane] = expf(static_cast<float>(x));
-            vec[kChunk + lane] = expf(static_cast<float>(last - x));
-            vec[2 * kChunk + lane] = beta;
-            if constexpr (kBack) a.gsum[(static_cast<int64_t>(place) * a.s.Hv + h) * kChunk + lane] = x;
+            const int64_t ph = static_cast<int64_t>(place) * a.s.Hv + h;
+            const auto put = [&](char *block) {
+                float *vec = reinterpret_cast<float *>(block);
+                vec[lane] = expf(static_cast<float>(x));
+                vec[kChunk + lane] = expf(static_cast<float>(last - x));
+                vec[2 * kChunk + lane] = beta;
+            };
+            put(a.within + ph * kBlock + kBlock - 1024);
+            if constexpr (kBack) {
+                put(a.back + ph * kBackBlock + kBackBlock - 1024);
+                a.gsum[ph * kChunk + lane] = x;
+            }
         }
         __syncthreads();
 #pragma unroll
@@ -196,7 +203,7 @@ __global__ __launch_bounds__(256) void k_prep(PrepArgs a) {
                     }
                     *reinterpret_cast<f4 *>(&As[x][block_of(wave, jt)][r * 16 + 4 * g]) = av;
                 }
-            char *P = a.P + ph * (kPBlocks * 1024 * NO) + lane * 16;
+            char *P = a.within + ph * kBlock + kTBytes + lane * 16;
 #pragma unroll
             for (int half = 0; half < 2; ++half)
                 if (half <= wave / 2) {
@@ -210,7 +217,7 @@ __global__ __launch_bounds__(256) void k_prep(PrepArgs a) {
                 // operand (jt, half): lane r token j, eight tokens i of the tiles 2 half
                 // and 2 half + 1; this wave's four of them.  Operands whose tiles lie
                 // all above the diagonal do not exist.
-                char *Pn = a.Pn + ph * (kPBlocks * 1024 * 3) + lane * 16 + 8 * (wave & 1);
+                char *Pn = a.back + ph * kBackBlock + kTBytes + lane * 16 + 8 * (wave & 1);
 #pragma unroll
                 for (int jt = 0; jt < 4; ++jt) {
                     if (jt / 2 > wave / 2) continue;
@@ -254,8 +261,8 @@ __global__ __launch_bounds__(256) void k_prep(PrepArgs a) {
         if (h0 + x < group) {
             const int h = kh + (h0 + x) * a.s.Hk;
             const int64_t ph = static_cast<int64_t>(place) * a.s.Hv + h;
-            float *T = a.T + ph * (kTBlocks * 256) + lane * 4;
-            float *Tn = kBack ? a.Tn + ph * (kTBlocks * 256) + lane * 4 : nullptr;
+            float *T = reinterpret_cast<float *>(a.within + ph * kBlock) + lane * 4;
+            float *Tn = kBack ? reinterpret_cast<float *>(a.back + ph * kBackBlock) + lane * 4 : nullptr;
             const int j0 = wave < HB ? 0 : 1, j1 = wave < HB ? 1 : 4;
             for (int j = j0; j < j1; ++j) {
                 f4 col[4];                              // T_ij, lane r column r, rows 4 g..

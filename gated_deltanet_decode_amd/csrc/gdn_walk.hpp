@@ -43,7 +43,7 @@ __device__ __forceinline__ void fetch_rows(const ChunkArgs &a, char *K, char *Q,
 #pragma unroll
         for (int i = 0; i < 16 / W; ++i) {
             const int rr = (i * W + wave) * 4 + (lane >> 4);
-            const int off = rr * Hk * (kHeadDim * 2) + (((lane & 15) ^ (rr & 15)) << 4);
+            const int off = rr * Hk * (kHeadDim * 2) + (((lane & 15) ^ turn(rr)) << 4);
             fetch16(K + (i * W + wave) * 1024, static_cast<const char *>(a.k) + at, bytes, off, 0);
             fetch16(Q + (i * W + wave) * 1024, static_cast<const char *>(a.q) + at, bytes, off, 0);
         }
@@ -77,11 +77,21 @@ __device__ __forceinline__ u4 columns_of(const char *plane, int half, int t, int
     return u4{x.x, x.y, y.x, y.y};
 }
 
+// A chunk's operands in LDS: K and Q (NP planes each), and a block of k_prep.
 template <int NP, int NO>
 struct Stage {
     static constexpr int kK = 0, kQ = NP * kPlaneBytes, kT = 2 * NP * kPlaneBytes, kP = kT + kTBytes,
-                         kVec = kP + kPBlocks * 1024 * NO, kBytes = kVec + 1024;
+                         kVec = kP + kPBlocks * 1024 * NO, kBytes = kT + (within_bytes(NO) + 8191) / 8192 * 8192;
 };
+
+// `bytes` of a block on its way to LDS; each wave takes the same number of kilobytes,
+// and those past the end come as they may.
+template <int kBytes, int W>
+__device__ __forceinline__ void fetch_block(const char *block, char *to, int wave, int lane) {
+#pragma unroll
+    for (int i = 0; i < (kBytes / 1024 + W - 1) / W; ++i)
+        fetch16(to + (i * W + wave) * 1024, block, kBytes, (i * W + wave) * 1024 + lane * 16, 0);
+}
 
 // W waves, 16 rows of the state each.  NP planes of k and q, NO of what only the
 // outputs see; S buffers of a chunk's operands.  For the backward pass (kBack) the
@@ -91,6 +101,7 @@ template <typename ET, int NP, int NO, int W, int S, bool kBack>
 __global__ __launch_bounds__(64 * W) void k_walk(ChunkArgs a, int parts) {
     typedef typename ET::bits bits;
     typedef Stage<NP, NO> L;
+    constexpr int kAhead = NP == 1 ? 2 : 1;               // sets of K and Q operands in registers
     __shared__ alignas(1024) char buf0[L::kBytes], buf1[S > 1 ? L::kBytes : 16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
@@ -106,7 +117,7 @@ __global__ __launch_bounds__(64 * W) void k_walk(ChunkArgs a, int parts) {
     if (slot < 0) return;
     const Span sp = span_of(a.s, b);
     const int chunks = (sp.len + kChunk - 1) / kChunk;
-    const int dv = (part * W + wave) * 16 + r;           // this lane's row of M
+    const int dv0 = (part * W + wave) * 16, dv = dv0 + r;   // this lane's row of M
 
     // M[dv][32 jj + 8 g + 0..7] are the four of tile 2 jj and the four of 2 jj + 1
     f4 M[8];
@@ -117,35 +128,24 @@ __global__ __launch_bounds__(64 * W) void k_walk(ChunkArgs a, int parts) {
 
     const int place0 = place_of(sp.first, b);
     auto fetch = [&](char *to, int c) {
-        const int64_t place = place0 + c, ph = place * Hv + h;
+        const int64_t place = place0 + c;
         const int rows = min(kChunk, sp.len - c * kChunk);
         fetch_rows<ET, NP, W>(a, to + L::kK, to + L::kQ, place, sp.first + c * kChunk, rows, kh, wave, lane);
-        const float *T = a.T + ph * (kTBlocks * 256);
-        const char *P = a.P + ph * (kPBlocks * 1024 * NO);
-        for (int i = wave; i < kTBlocks + kPBlocks * NO + 1; i += W) {
-            if (i < kTBlocks)
-                fetch16(to + L::kT + i * 1024, T, kTBytes, lane * 16, i * 1024);
-            else if (i < kTBlocks + kPBlocks * NO)
-                fetch16(to + L::kP + (i - kTBlocks) * 1024, P, kPBlocks * 1024 * NO, lane * 16, (i - kTBlocks) * 1024);
-            else
-                fetch16(to + L::kVec, a.vec + ph * kVecFloats, kVecFloats * 4, lane * 16, 0);
-        }
+        fetch_block<within_bytes(NO), W>(a.within + (place * Hv + h) * within_bytes(NO), to + L::kT, wave, lane);
     };
-    const bits *vp = static_cast<const bits *>(a.v) + (static_cast<int64_t>(sp.first) * Hv + h) * kHeadDim + dv;
-    bits *op = static_cast<bits *>(a.out) + (static_cast<int64_t>(sp.first) * Hv + h) * kHeadDim + dv - r + 4 * g;
-    const bits *dop = static_cast<const bits *>(a.d_out) + (static_cast<int64_t>(sp.first) * Hv + h) * kHeadDim + dv - r + 4 * g;
-    const int64_t vstride = static_cast<int64_t>(Hv) * kHeadDim;
+    auto rows_of = [&](const void *base, int c) {
+        return Rows<ET>(base, static_cast<int64_t>(sp.first) + c * kChunk, min(kChunk, sp.len - c * kChunk), h, Hv);
+    };
     bits vn[16];                                          // v of the chunk to come
     auto load_v = [&](int c) {
+        const Rows<ET> v = rows_of(a.v, c);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int t = c * kChunk + 16 * (i / 4) + 4 * g + i % 4;
-            vn[i] = t < sp.len ? vp[t * vstride] : bits(0);
-        }
+        for (int i = 0; i < 16; ++i) vn[i] = v.load(16 * (i / 4) + 4 * g + i % 4, dv);
     };
 
     auto chunk = [&](char *cur, char *nxt, int c) {
         const int64_t ph = (static_cast<int64_t>(place0) + c) * Hv + h;
+        const int rows = min(kChunk, sp.len - c * kChunk);
         if constexpr (kBack) {
             float *to = a.states + ph * (kHeadDim * kHeadDim) + dv * kHeadDim + 8 * g;
 #pragma unroll
@@ -154,34 +154,43 @@ __global__ __launch_bounds__(64 * W) void k_walk(ChunkArgs a, int parts) {
         if (S == 1) {
             meet();                                       // the buffer is read
             fetch(cur, c);
+            wait_all<0>();
+        } else {
+            // This chunk's fetches have landed; what came behind them may still be on
+            // its way: the 16 loads of v at least, and for the backward pass 16 stores
+            // of corrections.
+            wait_all<kBack ? 32 : 16>();
         }
-        wait_all<0>();
-        const int rows = min(kChunk, sp.len - c * kChunk);
         clear_rows<NP, W>(cur + L::kK, cur + L::kQ, rows);
         meet();                                           // cur has landed, nxt is read
         if (S > 1 && c + 1 < chunks) fetch(nxt, c + 1);
+        // K and Q against the state, 32 dk at a time, the next ones read ahead
         f4 Y[4] = {}, Z[4] = {};
+        u4 kf[kAhead][4][NP], qf[kAhead][4][NP];
+        auto read = [&](int jj) {
+#pragma unroll
+            for (int jt = 0; jt < 4; ++jt)
+#pragma unroll
+                for (int p = 0; p < NP; ++p) {
+                    const int at = p * kPlaneBytes + plane_at(jt * 16 + r, 4 * jj + g);
+                    kf[jj % kAhead][jt][p] = *reinterpret_cast<const u4 *>(cur + L::kK + at);
+                    qf[jj % kAhead][jt][p] = *reinterpret_cast<const u4 *>(cur + L::kQ + at);
+                }
+        };
+        if (kAhead > 1) read(0);
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) {
+            if (kAhead == 1) read(jj);
+            else if (jj < 3) read(jj + 1);
             u4 m3[3], mo[NO];
             planes_of<3>(M[2 * jj], M[2 * jj + 1], m3);
 #pragma unroll
             for (int p = 0; p < NO; ++p) mo[p] = m3[p];
-#pragma unroll
-            for (int jt = 0; jt < 4; ++jt) {
-                u4 kf[NP], qf[NP];
-#pragma unroll
-                for (int p = 0; p < NP; ++p) {
-                    const int at = p * kPlaneBytes + plane_at(jt * 16 + r, 4 * jj + g);
-                    kf[p] = *reinterpret_cast<const u4 *>(cur + L::kK + at);
-                    qf[p] = *reinterpret_cast<const u4 *>(cur + L::kQ + at);
-                }
-                Y[jt] = mma_planes<2>(kf, m3, Y[jt]);                 // token 4 g + e, row dv
-                Z[jt] = mma_planes<NO - 1>(mo, qf, Z[jt]);            // dv 4 g + e, token r
-            }
+            mma_planes<2, true>(kf[jj % kAhead], m3, Y);              // token 4 g + e, row dv
+            mma_planes<NO - 1, false>(qf[jj % kAhead], mo, Z);        // dv 4 g + e, token r
         }
         const float *vec = reinterpret_cast<const float *>(cur + L::kVec);
-        f4 X[4], E[4];
+        f4 X[4], E[4] = {};
 #pragma unroll
         for (int jt = 0; jt < 4; ++jt) {
             const f4 rise = *reinterpret_cast<const f4 *>(vec + 16 * jt + 4 * g);
@@ -191,23 +200,33 @@ __global__ __launch_bounds__(64 * W) void k_walk(ChunkArgs a, int parts) {
                 X[jt][e] = beta[e] * fmaf(-rise[e], Y[jt][e], ET::get(vn[4 * jt + e]));
         }
         if (c + 1 < chunks) load_v(c + 1);
+        // Delta: token 4 g + e, row dv
 #pragma unroll
-        for (int it = 0; it < 4; ++it) {
-            f4 d = {0, 0, 0, 0};
+        for (int jt = 0; jt < 4; ++jt) {
+            f4 tf[4];
 #pragma unroll
-            for (int jt = 0; jt <= it; ++jt)
-                d = mma32(*reinterpret_cast<const f4 *>(cur + L::kT + block_of(it, jt) * 1024 + lane * 16), X[jt], d);
-            E[it] = d;                                    // Delta: token 4 g + e, row dv
-            if constexpr (kBack) {
-                float *to = a.delta + (ph * kChunk + 16 * it + 4 * g) * kHeadDim + dv;
+            for (int it = jt; it < 4; ++it)
+                tf[it] = *reinterpret_cast<const f4 *>(cur + L::kT + block_of(it, jt) * 1024 + lane * 16);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) to[e * kHeadDim] = d[e];
-            }
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int it = jt; it < 4; ++it)
+                    E[it] = __builtin_amdgcn_mfma_f32_16x16x4f32(tf[it][s], X[jt][s], E[it], 0, 0, 0);
+        }
+        if constexpr (kBack) {
+            float *to = a.delta + (ph * kChunk + 4 * g) * kHeadDim + dv;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) to[(16 * (i / 4) + i % 4) * kHeadDim] = E[i / 4][i % 4];
         }
         // outputs
         u4 dp[2][NO];
         planes_of<NO>(E[0], E[1], dp[0]);
         planes_of<NO>(E[2], E[3], dp[1]);
+        const Rows<ET> out = rows_of(kBack ? a.d_out : a.out, c);
+        f4 dout[4];
+        if constexpr (kBack)
+#pragma unroll
+            for (int it = 0; it < 4; ++it) dout[it] = out.load4(16 * it + r, dv0 + 4 * g);
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
             f4 o = Z[it] * (kReadScale * vec[16 * it + r]);
@@ -220,22 +239,15 @@ __global__ __launch_bounds__(64 * W) void k_walk(ChunkArgs a, int parts) {
                                                           lane * 16);
                 o = mma_planes<NO - 1>(dp[half], pf, o);
             }
-            const int t = c * kChunk + 16 * it + r;
             if constexpr (kBack) {
-                float s = 0.0f;
-                if (t < sp.len) {
-                    const auto w = Pack<bits, 4>::load(dop + t * vstride);
+                float s = 0.0f;                           // d_out is zero past the last token
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s = fmaf(o[e], ET::get(w[e]), s);
-                }
+                for (int e = 0; e < 4; ++e) s = fmaf(o[e], dout[it][e], s);
                 s += __shfl_xor(s, 16);
                 s += __shfl_xor(s, 32);
                 if (g == 0) a.od[(ph * 8 + part * W + wave) * kChunk + 16 * it + r] = s;
-            } else if (t < sp.len) {
-                typename Pack<bits, 4>::vec w;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = ET::put(o[e]);
-                Pack<bits, 4>::store(op + t * vstride, w);
+            } else {
+                out.store4(16 * it + r, dv0 + 4 * g, o);
             }
         }
         // the state
@@ -246,20 +258,19 @@ __global__ __launch_bounds__(64 * W) void k_walk(ChunkArgs a, int parts) {
         for (int t = 0; t < 8; ++t) M[t] *= all;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            u4 ep[3];
+            u4 ep[3], kt[8][NP];
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int p = 0; p < NP; ++p) kt[t][p] = columns_of(cur + L::kK + p * kPlaneBytes, half, t, r, g);
             planes_of<3>(E[2 * half], E[2 * half + 1], ep);
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                u4 kt[NP];
-#pragma unroll
-                for (int p = 0; p < NP; ++p) kt[p] = columns_of(cur + L::kK + p * kPlaneBytes, half, t, r, g);
-                M[t] = mma_planes<2>(kt, ep, M[t]);
-            }
+            mma_planes<2, true>(kt, ep, M);
         }
     };
     if (chunks > 0) {
-        load_v(0);
         if (S > 1) fetch(buf0, 0);
+        load_v(0);
+        wait_all<0>();
         int c = 0;
         if constexpr (S > 1) {
             for (; c + 2 <= chunks; c += 2) {
@@ -277,13 +288,23 @@ __global__ __launch_bounds__(64 * W) void k_walk(ChunkArgs a, int parts) {
     }
 }
 
-template <typename ET, int NP, int NO, int S, bool kBack>
-hipError_t launch_walk(const ChunkArgs &a, hipStream_t s) {
-    constexpr int W = 8;
+// As many waves a workgroup (of 16 rows of a head's 128) as leave each compute unit
+// one: a wave alone on its SIMD goes through a chunk twice as fast as two of them.
+template <typename ET, int NP, int NO, int W, int S, bool kBack>
+hipError_t launch_walk_of(const ChunkArgs &a, hipStream_t s) {
     const int parts = 8 / W;
     const int64_t wgs = static_cast<int64_t>(a.s.B) * a.s.Hv * parts;
     k_walk<ET, NP, NO, W, S, kBack><<<dim3(static_cast<unsigned>((wgs + 7) / 8 * 8)), dim3(64 * W), 0, s>>>(a, parts);
     return hipGetLastError();
+}
+template <typename ET, int NP, int NO, int S, bool kBack>
+hipError_t launch_walk(const ChunkArgs &a, hipStream_t s) {
+    const int64_t heads = static_cast<int64_t>(a.s.B) * a.s.Hv;
+    const int cus = device_cus();
+    if (heads * 8 <= cus) return launch_walk_of<ET, NP, NO, 1, S, kBack>(a, s);
+    if (heads * 4 <= cus) return launch_walk_of<ET, NP, NO, 2, S, kBack>(a, s);
+    if (heads * 2 <= cus) return launch_walk_of<ET, NP, NO, 4, S, kBack>(a, s);
+    return launch_walk_of<ET, NP, NO, 8, S, kBack>(a, s);
 }
 
 }  // namespace
