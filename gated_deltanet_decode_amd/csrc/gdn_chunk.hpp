@@ -38,15 +38,15 @@ constexpr int planes_out(int type) { return type == 0 ? 3 : 2; }
 
 // What a chunk's tokens do to each other, a block per chunk place and value head, as
 // LDS holds it:
-//   T    (I + A)^-1, its ten lower blocks of 16 x 16 floats, each in the order in
-//        which the lanes of a wave read it as an operand;
-//   P    the masked, decayed and scaled Q K^T in bf16 planes: six operands of 16
-//        tokens x 32 tokens each;
+//   T    (I + A)^-1 in three bf16 planes: six operands of 16 tokens x 32 tokens each
+//        (the others lie above the diagonal);
+//   P    the masked, decayed and scaled Q K^T, likewise, in as many planes as the
+//        outputs need;
 //   vec  rise, fall and beta of the 64 tokens.
 // And, unless the inputs are bf16, the planes of k and q per chunk place and key
 // head.
-constexpr int kTBlocks = 10, kPBlocks = 6;
-constexpr int kTBytes = kTBlocks * 1024;
+constexpr int kPBlocks = 6;
+constexpr int kTBytes = kPBlocks * 1024 * 3;
 constexpr int kVecFloats = 3 * kChunk;
 constexpr int within_bytes(int planes) { return kTBytes + kPBlocks * 1024 * planes + 1024; }
 

@@ -77,6 +77,7 @@ template <typename ET, int NP, int W, int S>
 __global__ __launch_bounds__(64 * W) void k_back(BackArgs a, int parts) {
     typedef typename ET::bits bits;
     typedef Stage<NP, 3> L;
+    constexpr int kAhead = NP == 1 ? 2 : 1;
     __shared__ alignas(1024) char buf0[L::kBytes], buf1[S > 1 ? L::kBytes : 16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
@@ -138,19 +139,23 @@ __global__ __launch_bounds__(64 * W) void k_back(BackArgs a, int parts) {
         if (S > 1 && c > 0) fetch(nxt, c - 1);
         const float *vec = reinterpret_cast<const float *>(cur + L::kVec);
         f4 U[4] = {};
+        u4 kf[kAhead][4][NP];
+        auto read = [&](int jj) {
 #pragma unroll
-        for (int jj = 0; jj < 4; ++jj) {
-            u4 g3[3];
-            planes_of<3>(G[2 * jj], G[2 * jj + 1], g3);
-#pragma unroll
-            for (int jt = 0; jt < 4; ++jt) {
-                u4 kf[NP];
+            for (int jt = 0; jt < 4; ++jt)
 #pragma unroll
                 for (int p = 0; p < NP; ++p)
-                    kf[p] = *reinterpret_cast<const u4 *>(cur + L::kK + p * kPlaneBytes +
-                                                          plane_at(jt * 16 + r, 4 * jj + g));
-                U[jt] = mma_planes<2>(kf, g3, U[jt]);
-            }
+                    kf[jj % kAhead][jt][p] = *reinterpret_cast<const u4 *>(cur + L::kK + p * kPlaneBytes +
+                                                                           plane_at(jt * 16 + r, 4 * jj + g));
+        };
+        if (kAhead > 1) read(0);
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+            if (kAhead == 1) read(jj);
+            else if (jj < 3) read(jj + 1);
+            u4 g3[3];
+            planes_of<3>(G[2 * jj], G[2 * jj + 1], g3);
+            mma_planes<2, true>(kf[jj % kAhead], g3, U);
         }
         u4 op[2][NP];
         planes_in<ET, NP>(on, op[0]);
@@ -166,25 +171,28 @@ __global__ __launch_bounds__(64 * W) void k_back(BackArgs a, int parts) {
 #pragma unroll
             for (int half = jt / 2; half < 2; ++half) {
                 u4 pf[3];
-#pragma unroll
-                for (int m = 0; m < 3; ++m)
-                    pf[m] = *reinterpret_cast<const u4 *>(cur + L::kP + (m * kPBlocks + pnblock_of(jt, half)) * 1024 +
-                                                          lane * 16);
+                operand_at<3>(cur + L::kP, pnblock_of(jt, half), lane, pf);
                 dd[jt] = mma_planes<2>(pf, op[half], dd[jt]);
             }
         }
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) du += __shfl_xor(du, d);
         if (lane == 0) a.du[ph * 8 + part * W + wave] = du;
-        f4 R[4];
+        f4 R[4] = {};
+        u4 tf[4][3], xp[3];
+#pragma unroll
+        for (int jt = 0; jt < 4; ++jt) operand_at<3>(cur + L::kT, pnblock_of(jt, 1), lane, tf[jt]);
+        planes_of<3>(dd[2], dd[3], xp);
+        mma_planes<2, true>(tf, xp, R);
+        u4 te[2][3];
+#pragma unroll
+        for (int jt = 0; jt < 2; ++jt) operand_at<3>(cur + L::kT, pnblock_of(jt, 0), lane, te[jt]);
+        planes_of<3>(dd[0], dd[1], xp);
+        f4 (&R0)[2] = *reinterpret_cast<f4 (*)[2]>(&R[0]);
+        mma_planes<2, true>(te, xp, R0);
         const Rows<ET> dvr = rows_of(a.dv, c);
 #pragma unroll
         for (int jt = 0; jt < 4; ++jt) {
-            R[jt] = f4{0, 0, 0, 0};
-#pragma unroll
-            for (int it = jt; it < 4; ++it)
-                R[jt] = mma32(*reinterpret_cast<const f4 *>(cur + L::kT + block_of(it, jt) * 1024 + lane * 16), dd[it],
-                              R[jt]);
             const f4 beta = *reinterpret_cast<const f4 *>(vec + 2 * kChunk + 16 * jt + 4 * g);
             float *to = a.r + (ph * kChunk + 16 * jt + 4 * g) * kHeadDim + dv;
 #pragma unroll
@@ -213,17 +221,17 @@ __global__ __launch_bounds__(64 * W) void k_back(BackArgs a, int parts) {
             u4 po[3], pv[3];
             planes_of<3>(xo[0], xo[1], po);
             planes_of<3>(xv[0], xv[1], pv);
+            u4 ct[8][NP];
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                u4 qt[NP], kt[NP];
+            for (int t = 0; t < 8; ++t)
 #pragma unroll
-                for (int p = 0; p < NP; ++p) {
-                    qt[p] = columns_of(cur + L::kQ + p * kPlaneBytes, half, t, r, g);
-                    kt[p] = columns_of(cur + L::kK + p * kPlaneBytes, half, t, r, g);
-                }
-                G[t] = mma_planes<2>(qt, po, G[t]);
-                G[t] = mma_planes<2>(kt, pv, G[t]);
-            }
+                for (int p = 0; p < NP; ++p) ct[t][p] = columns_of(cur + L::kQ + p * kPlaneBytes, half, t, r, g);
+            mma_planes<2, true>(ct, po, G);
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int p = 0; p < NP; ++p) ct[t][p] = columns_of(cur + L::kK + p * kPlaneBytes, half, t, r, g);
+            mma_planes<2, true>(ct, pv, G);
         }
         if (c > 0) load_o(c - 1);
     };

@@ -42,6 +42,7 @@ struct PrepArgs {
 __device__ __forceinline__ int turn(int row) { return (row & 3) << 2 | (row >> 2 & 3); }
 __device__ __forceinline__ int plane_at(int row, int chunk) { return row * 256 + ((chunk ^ turn(row)) << 4); }
 
+constexpr int kABlocks = 10;
 constexpr int block_of(int it, int jt) { return it * (it + 1) / 2 + jt; }
 // Operand of 16 tokens it x 32 tokens of half h.
 constexpr int pblock_of(int it, int h) { return it < 2 ? it : 2 + (it - 2) * 2 + h; }
@@ -85,11 +86,15 @@ __device__ __forceinline__ float beta_of(float x) {
 // tokens w of the chunk as its rows.  The value heads of the key head go through
 // two at a time.
 template <typename ET, int NP, int NO, bool kBack>
-__global__ __launch_bounds__(256) void k_prep(PrepArgs a) {
+__global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : kBack ? 3 : 4) void k_prep(PrepArgs a) {
     constexpr int HB = 2;
     constexpr int kBlock = within_bytes(NO), kBackBlock = within_bytes(3);
-    __shared__ alignas(16) char kp[NP][kPlaneBytes], qp[NP][kPlaneBytes];
-    __shared__ alignas(16) float As[HB][kTBlocks][256], Td[HB][4][256];
+    // the planes of k and q; after their products A's blocks and T's diagonal ones
+    __shared__ alignas(16) char lds[2 * NP * kPlaneBytes];
+    char (*const kp)[kPlaneBytes] = reinterpret_cast<char (*)[kPlaneBytes]>(lds), (*const qp)[kPlaneBytes] = kp + NP;
+    float (*const As)[kABlocks][256] = reinterpret_cast<float (*)[kABlocks][256]>(lds);
+    float (*const Td)[4][256] = reinterpret_cast<float (*)[4][256]>(lds + HB * kABlocks * 1024);
+    static_assert(HB * (kABlocks * 1024 + 4096) <= sizeof(lds), "");
     __shared__ double gs[HB][kChunk];
     __shared__ float bs[HB][kChunk];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -153,7 +158,7 @@ __global__ __launch_bounds__(256) void k_prep(PrepArgs a) {
     }
     const int group = a.s.Hv / a.s.Hk;
     for (int h0 = 0; h0 < group; h0 += HB) {
-        if (h0 > 0) __syncthreads();                    // the last heads' columns are done
+        __syncthreads();                                // the planes, the last heads' columns are read
         if (wave < HB && h0 + wave < group) {           // running sums of the gates
             const int h = kh + (h0 + wave) * a.s.Hk;
             const int64_t at = (t0 + lane) * a.s.Hv + h;
@@ -261,29 +266,46 @@ __global__ __launch_bounds__(256) void k_prep(PrepArgs a) {
         if (h0 + x < group) {
             const int h = kh + (h0 + x) * a.s.Hk;
             const int64_t ph = static_cast<int64_t>(place) * a.s.Hv + h;
-            float *T = reinterpret_cast<float *>(a.within + ph * kBlock) + lane * 4;
-            float *Tn = kBack ? reinterpret_cast<float *>(a.back + ph * kBackBlock) + lane * 4 : nullptr;
+            char *const T = a.within + ph * kBlock + lane * 16;
+            // rows: T_ij with lane r row r, elements columns 4 g..: the half (j & 1) of an
+            // operand of row tile i
+            const auto put_rows = [&](int i, int j, f4 rows) {
+                u4 p[3];
+                planes_of<3>(rows, rows, p);
+#pragma unroll
+                for (int m = 0; m < 3; ++m)
+                    *reinterpret_cast<u2 *>(T + (m * kPBlocks + pblock_of(i, j / 2)) * 1024 + 8 * (j & 1)) = u2{p[m].x, p[m].y};
+            };
             const int j0 = wave < HB ? 0 : 1, j1 = wave < HB ? 1 : 4;
-            for (int j = j0; j < j1; ++j) {
-                f4 col[4];                              // T_ij, lane r column r, rows 4 g..
 #pragma unroll
-                for (int e = 0; e < 4; ++e) col[0][e] = Td[x][j][(4 * g + e) * 16 + r];
-                *reinterpret_cast<f4 *>(T + block_of(j, j) * 256) =
-                    *reinterpret_cast<const f4 *>(&Td[x][j][r * 16 + 4 * g]);
-                if constexpr (kBack) *reinterpret_cast<f4 *>(Tn + block_of(j, j) * 256) = col[0];
+            for (int j = 0; j < 4; ++j) {
+                if (j < j0 || j >= j1) continue;
+                f4 col[4] = {};                         // T_ij, lane r column r, rows 4 g..
 #pragma unroll
-                for (int d = 1; d < 4; ++d) {
-                    const int i = j + d;
-                    if (i > 3) break;
+                for (int e = 0; e < 4; ++e) col[j][e] = Td[x][j][(4 * g + e) * 16 + r];
+                put_rows(j, j, *reinterpret_cast<const f4 *>(&Td[x][j][r * 16 + 4 * g]));
+                if (j & 1) put_rows(j - 1, j, f4{0, 0, 0, 0});
+#pragma unroll
+                for (int i = j + 1; i < 4; ++i) {
                     f4 s = {0, 0, 0, 0};
 #pragma unroll
-                    for (int m = 0; m < d; ++m)
-                        s = mma32(*reinterpret_cast<const f4 *>(&As[x][block_of(i, j + m)][r * 16 + 4 * g]), col[m], s);
+                    for (int m = j; m < i; ++m)
+                        s = mma32(*reinterpret_cast<const f4 *>(&As[x][block_of(i, m)][r * 16 + 4 * g]), col[m], s);
                     s = -s;
                     const f4 diag = *reinterpret_cast<const f4 *>(&Td[x][i][r * 16 + 4 * g]);
-                    col[d] = mma32(diag, s, f4{0, 0, 0, 0});
-                    *reinterpret_cast<f4 *>(T + block_of(i, j) * 256) = mma32(s, diag, f4{0, 0, 0, 0});
-                    if constexpr (kBack) *reinterpret_cast<f4 *>(Tn + block_of(i, j) * 256) = col[d];
+                    col[i] = mma32(diag, s, f4{0, 0, 0, 0});
+                    put_rows(i, j, mma32(s, diag, f4{0, 0, 0, 0}));
+                }
+                if constexpr (kBack) {
+                    char *const Tn = a.back + ph * kBackBlock + lane * 16;
+#pragma unroll
+                    for (int half = j / 2; half < 2; ++half) {
+                        u4 p[3];
+                        planes_of<3>(col[2 * half], col[2 * half + 1], p);
+#pragma unroll
+                        for (int m = 0; m < 3; ++m)
+                            *reinterpret_cast<u4 *>(Tn + (m * kPBlocks + pnblock_of(j, half)) * 1024) = p[m];
+                    }
                 }
             }
         }

@@ -84,6 +84,13 @@ struct Stage {
                          kVec = kP + kPBlocks * 1024 * NO, kBytes = kT + (within_bytes(NO) + 8191) / 8192 * 8192;
 };
 
+// The planes of operand `block` of T or P.
+template <int N>
+__device__ __forceinline__ void operand_at(const char *at, int block, int lane, u4 (&p)[N]) {
+#pragma unroll
+    for (int m = 0; m < N; ++m) p[m] = *reinterpret_cast<const u4 *>(at + (m * kPBlocks + block) * 1024 + lane * 16);
+}
+
 // `bytes` of a block on its way to LDS; each wave takes the same number of kilobytes,
 // and those past the end come as they may.
 template <int kBytes, int W>
@@ -201,18 +208,17 @@ __global__ __launch_bounds__(64 * W) void k_walk(ChunkArgs a, int parts) {
         }
         if (c + 1 < chunks) load_v(c + 1);
         // Delta: token 4 g + e, row dv
+        u4 tf[4][3], xp[3];
 #pragma unroll
-        for (int jt = 0; jt < 4; ++jt) {
-            f4 tf[4];
+        for (int it = 0; it < 4; ++it) operand_at<3>(cur + L::kT, pblock_of(it, 0), lane, tf[it]);
+        planes_of<3>(X[0], X[1], xp);
+        mma_planes<2, true>(tf, xp, E);
+        u4 te[2][3];
 #pragma unroll
-            for (int it = jt; it < 4; ++it)
-                tf[it] = *reinterpret_cast<const f4 *>(cur + L::kT + block_of(it, jt) * 1024 + lane * 16);
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-#pragma unroll
-                for (int it = jt; it < 4; ++it)
-                    E[it] = __builtin_amdgcn_mfma_f32_16x16x4f32(tf[it][s], X[jt][s], E[it], 0, 0, 0);
-        }
+        for (int it = 0; it < 2; ++it) operand_at<3>(cur + L::kT, pblock_of(it + 2, 1), lane, te[it]);
+        planes_of<3>(X[2], X[3], xp);
+        f4 (&E2)[2] = *reinterpret_cast<f4 (*)[2]>(&E[2]);
+        mma_planes<2, true>(te, xp, E2);
         if constexpr (kBack) {
             float *to = a.delta + (ph * kChunk + 4 * g) * kHeadDim + dv;
 #pragma unroll
@@ -233,10 +239,7 @@ __global__ __launch_bounds__(64 * W) void k_walk(ChunkArgs a, int parts) {
 #pragma unroll
             for (int half = 0; half <= it / 2; ++half) {
                 u4 pf[NO];
-#pragma unroll
-                for (int m = 0; m < NO; ++m)
-                    pf[m] = *reinterpret_cast<const u4 *>(cur + L::kP + (m * kPBlocks + pblock_of(it, half)) * 1024 +
-                                                          lane * 16);
+                operand_at<NO>(cur + L::kP, pblock_of(it, half), lane, pf);
                 o = mma_planes<NO - 1>(dp[half], pf, o);
             }
             if constexpr (kBack) {

@@ -41,7 +41,7 @@ def decode(g, x, state_out="new"):
     return out, x["state"] if so is None else so
 
 
-def check(x, out, so, dtype):
+def check(x, out, so, dtype, more=1):
     y, pool, size, psize = rr.forward(x)
     used = x["offsets"][-1].item()
     o = out.cpu().double()
@@ -54,7 +54,7 @@ def check(x, out, so, dtype):
     bound = rr.state_bound(psize)
     assert ((s - pool).abs() <= bound)[live].all(), float(((s - pool).abs() / bound)[live].max())
     if live.any():
-        assert rr.rel(s[live], pool[live]) <= 2.0 ** -20   # roundings of 2^-24, some hundreds, independent
+        assert rr.rel(s[live], pool[live]) <= more * 2.0 ** -20   # roundings of 2^-24, some hundreds, independent
     assert (s[~live] == 5.0).all()                        # slots of no sequence
 
 
@@ -91,11 +91,14 @@ def test_chunk_one_strong_decay(g, dtype):
 
 def test_chunk_same_key_and_full_writes(g):
     """Keys that are all alike and beta 1: the triangular system is as full as it
-    gets, every token replaces what the one before it wrote."""
+    gets, every token replaces what the one before it wrote.  The corrections are
+    v_j - v_(j-1), of norm sqrt(2) |v|, and their sum over 128 tokens, of norm |v|,
+    carries the independent roundings of all of them: sqrt(2 * 128) = 16 times one's
+    where a sum that does not cancel has its own size."""
     x = rr.inputs([128], 2, 1, torch.float32, 5, gate=0.0)
     x["k"][:] = x["k"][0]
     x["beta"][:] = 1.0
-    check(x, *chunk(g, x), torch.float32)
+    check(x, *chunk(g, x), torch.float32, more=16)
 
 
 @pytest.mark.parametrize("call", ["chunk", "decode"])
