@@ -35,41 +35,43 @@ __device__ __forceinline__ void planes_in(const typename ET::bits *x, u4 (&p)[NP
     }
 }
 
-// Columns dk 16 t + r of a plane as an operand: k are the tokens as in columns_of
-// (plain_columns), or the rows 8 g + e of a slab of 32.
-__device__ __forceinline__ u4 plain_columns(const char *plane, int half, int t, int r, int g) {
-    const int tok = 32 * half + 4 * g + (r >> 2), chunk = 2 * t + (r >> 1 & 1);
-    const u2 x = read_columns(plane + plane_at(tok, chunk) + 8 * (r & 1));
-    const u2 y = read_columns(plane + plane_at(tok + 16, chunk) + 8 * (r & 1));
+// Columns dk 16 t + r of a plane as an operand whose k are the tokens as in
+// columns_of.  turn() is the same for rows 16 apart, so that a lane needs one place
+// for each t.
+__device__ __forceinline__ int plain_place(int r, int g) {
+    return plane_at(4 * g + (r >> 2), r >> 1 & 1) + 8 * (r & 1);
+}
+__device__ __forceinline__ u4 plain_columns(const char *plane, int half, int t, int place) {
+    const char *at = plane + (place ^ t << 5) + half * 32 * 256;
+    const u2 x = read_columns(at), y = read_columns(at + 16 * 256);
     return u4{x.x, x.y, y.x, y.y};
 }
-__device__ __forceinline__ u4 slab_columns(const char *plane, int t, int r, int g) {
-    const int row = 8 * g + (r >> 2), chunk = 2 * t + (r >> 1 & 1);
-    const u2 x = read_columns(plane + plane_at(row, chunk) + 8 * (r & 1));
-    const u2 y = read_columns(plane + plane_at(row + 4, chunk) + 8 * (r & 1));
+// The same whose k are the rows 8 g + e of a slab of 32.
+__device__ __forceinline__ int slab_place(int r, int g) {
+    return plane_at(8 * g + (r >> 2), r >> 1 & 1) + 8 * (r & 1);
+}
+__device__ __forceinline__ u4 slab_columns(const char *plane, int t, int place) {
+    const u2 x = read_columns(plane + (place ^ t << 5)), y = read_columns(plane + (place ^ (t << 5 | 16)) + 4 * 256);
     return u4{x.x, x.y, y.x, y.y};
+}
+// Keeps what is derived from x from being formed ahead of a loop and spilled there.
+__device__ __forceinline__ int here(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
 }
 
-// The planes of a chunk's k, then q, to LDS, zero past its n tokens; ends with a
-// barrier.
-template <typename ET, int NP>
-__device__ __forceinline__ void load_kq(const ChunkArgs &a, char *to, int place, int64_t t0, int n, int kh) {
-    const char *kq = a.kq + (static_cast<int64_t>(place) * a.s.Hk + kh) * (2 * NP * kPlaneBytes);
-    for (int i = threadIdx.x; i < 2 * NP * kPlaneBytes / 16; i += 256) {
-        u4 x = {0, 0, 0, 0};
-        int at = i * 16;
-        if constexpr (NP == 1) {
-            const int row = i >> 4 & 63, chunk = i & 15;
-            at = (i >> 10) * kPlaneBytes + plane_at(row, chunk);
-            if (row < n)
-                x = *reinterpret_cast<const u4 *>(static_cast<const char *>(i < 1024 ? a.k : a.q) +
-                                                  ((t0 + row) * a.s.Hk + kh) * (kHeadDim * 2) + chunk * 16);
-        } else {
-            x = *reinterpret_cast<const u4 *>(kq + at);
-        }
-        *reinterpret_cast<u4 *>(to + at) = x;
+// The planes of a chunk's k (which = 0) or q to LDS, zero past its n tokens.
+template <typename ET, int NP, int kThreads>
+__device__ __forceinline__ void load_planes(const ChunkArgs &a, int which, char *to, int place, int64_t t0, int n, int kh) {
+    if constexpr (NP == 1) {
+        const Rows<ET> rows(which ? a.q : a.k, t0, n, kh, a.s.Hk);
+        for (int i = threadIdx.x; i < kPlaneBytes / 16; i += kThreads)
+            *reinterpret_cast<u4 *>(to + plane_at(i >> 4, i & 15)) = rows.load8(i >> 4, 8 * (i & 15)).x[0];
+    } else {
+        const char *kq = a.kq + ((static_cast<int64_t>(place) * a.s.Hk + kh) * 2 + which) * (NP * kPlaneBytes);
+        for (int i = threadIdx.x; i < NP * kPlaneBytes / 16; i += kThreads)
+            *reinterpret_cast<u4 *>(to + i * 16) = *reinterpret_cast<const u4 *>(kq + i * 16);
     }
-    __syncthreads();
 }
 
 // Along the sequences in reverse, 16 rows of G a wave as k_walk has rows of M.
@@ -257,27 +259,34 @@ __global__ __launch_bounds__(64 * W) void k_back(BackArgs a, int parts) {
 }
 
 // ------------------------------------------------------------ chunk by chunk
-// One workgroup of four waves per chunk place and key head, 16 tokens a wave, the
-// value heads that share the key head after each other.  The products over dv
-// run in slabs of 32: a wave's own rows of R, Delta and d_out come straight from
-// memory as operands, and through LDS for the other waves; the slabs of M and G
-// are cut into planes in LDS and read by columns.
+// One workgroup of eight waves per chunk place and key head, the value heads that
+// share the key head after each other.  Wave w + 4 p has the 16 tokens w as its
+// rows, and half p of the dk columns of dQ and dK; of the products between tokens it
+// forms F (p = 0) or E (p = 1), which change hands through LDS.  The products over
+// dv run in slabs of 32: a wave's own rows of R, Delta and d_out come straight
+// from memory as operands, and through LDS for the other waves; the slabs of M and G
+// are cut into planes in LDS and read by columns; the next slab, of the next head too,
+// is on its way meanwhile.  Cutting into planes and the matrix instructions bound it,
+// about half each; 8 ragged sequences of up to 4096 tokens, 32 value heads: 826 us
+// (four waves with whole rows of dk, products of rows scaled ahead: 1130).
 template <typename ET, int NP, int NO>
-__global__ __launch_bounds__(256) void k_grad(BackArgs a) {
-    typedef typename ET::bits bits;
+__global__ __launch_bounds__(512) void k_grad(BackArgs a) {
     constexpr int kRow = 64;                              // bytes of a token's slab of a plane
-    constexpr int kTok = kChunk * kRow;                   // bytes of a plane of R, Delta, d_out
+    constexpr int kTok = kChunk * kRow;                   // bytes of a plane of Delta, d_out or R
     constexpr int kMat = 32 * 256;                        // bytes of a plane of M or G
-    // the slabs, and after the last of them the planes of K and Q
-    constexpr int kSlab = (2 * NO + NP) * kTok + 2 * NO * kMat, kKQ = 2 * NP * kPlaneBytes;
-    __shared__ alignas(16) char lds[kSlab > kKQ ? kSlab : kKQ];
-    __shared__ double gs[kChunk];
-    __shared__ float vec[kVecFloats], dots[3][kChunk];
-    __shared__ double part[4];
-    char *const lr = lds, *const ld = lr + NO * kTok, *const lo = ld + NO * kTok, *const lm = lo + NP * kTok,
-         *const lg = lm + NO * kMat;
+    // K and Q stay, the operands F and E take the slabs' place; f32 reads Q anew for each
+    // head, to behind F and E.
+    constexpr int kK = NP * kPlaneBytes, kSlab = 3 * NO * kTok + 2 * NO * kMat, kPass = 20 * NO * 1024;
+    constexpr bool kStays = NP < 3;
+    constexpr int kTurn = kStays ? 2 * kK : kK, kQ = kStays ? kK : kK + kPass;
+    constexpr int kAll = kStays ? kTurn + (kSlab > kPass ? kSlab : kPass) : kTurn + (kSlab > kPass + kK ? kSlab : kPass + kK);
+    __shared__ alignas(16) char lds[kAll];
+    __shared__ double gs[kChunk], part[8];
+    __shared__ float vec[kVecFloats], dots[2][kChunk], ods[8][kChunk], dus[8];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r = lane & 15, g = lane >> 4;
+    const int r = lane & 15, g = lane >> 4, w = wave & 3, p = wave >> 2;
+    // LDS of Delta, of d_out or R, which is the half's own, of M and of G
+    char *const ld = lds + kTurn, *const lx = ld + (1 + p) * NO * kTok, *const lm = ld + 3 * NO * kTok, *const lg = lm + NO * kMat;
     const Packed &s = a.f.s;
     const int Hv = s.Hv, Hk = s.Hk;
     const int place = blockIdx.x / Hk, kh = blockIdx.x - place * Hk;
@@ -287,209 +296,275 @@ __global__ __launch_bounds__(256) void k_grad(BackArgs a) {
     if (c0 < 0 || c0 >= sp.len) return;
     const int n = min(kChunk, sp.len - c0);
     const int64_t t0 = sp.first + c0;
-    const int tok = wave * 16 + r;                        // this lane's token as a row or column
     // 16 bytes of four k of eight each: chunk c of row t at c ^ (t >> 1 & 3), which
     // spreads 16 rows over the banks twice
     const auto tok_at = [](int t, int c) { return t * kRow + ((c ^ (t >> 1 & 3)) << 4); };
+    // the planes of F to dQ, F to dK and E of a wave's tokens and one half of the others
+    // (the halves that are there)
+    const auto pass_at = [&](int lane, int which, int half, int m) {
+        const int unit = which == 0 ? w + 2 * half : which == 1 ? 6 + w + 4 * (1 - half) : 12 + 2 * w + half;
+        return ld + (unit * NO + m) * 1024 + lane * 16;
+    };
+    // (16-bit results round far above the hardware exponential's error)
+    const auto decay = [](double x) {
+        const float d = static_cast<float>(x);
+        return NO == 2 ? __builtin_amdgcn_exp2f(d * 1.44269504f) : expf(d);
+    };
 
-    f4 dq[8] = {}, dk[8] = {};                            // rows 16 wave + 4 g + e, column dk 16 t + r
-    for (int x = 0; x < Hv / Hk; ++x) {
-        const int h = kh + x * Hk;
+    f4 r0, r1, d0, d1, m0, m1, g0, g1;
+    typename Rows<ET>::Eight o, v;
+    double gx = 0.0;
+    float vx = 0.0f, odx, dux = 0.0f;
+    const auto load = [&](int h, int slab) {
+        const int lane = here(threadIdx.x) & 63, r = lane & 15, g = lane >> 4, tok = w * 16 + r;
         const int64_t ph = static_cast<int64_t>(place) * Hv + h;
-        if (x > 0) __syncthreads();                       // the last head is done with LDS
-        if (threadIdx.x < kChunk) gs[threadIdx.x] = a.gsum[ph * kChunk + threadIdx.x];
-        if (threadIdx.x < kVecFloats) vec[threadIdx.x] = reinterpret_cast<const float *>(
-            a.f.within + (ph + 1) * within_bytes(3) - 1024)[threadIdx.x];
-        f4 Z[8] = {}, Wm[8] = {}, H[8] = {};
-        // lane: own token; elements: the other's.  F1, E1 of tiles up to the own, F2, E2
-        // from it on.
-        f4 F1[4] = {}, E1[4] = {}, F2[4] = {}, E2[4] = {};
-        float rd = 0.0f, rv = 0.0f, gm = 0.0f;
-        const float *pr = a.r + (ph * kChunk + tok) * kHeadDim + 8 * g;
-        const float *pd = a.f.delta + (ph * kChunk + tok) * kHeadDim + 8 * g;
-        const int64_t vat = ((t0 + tok) * Hv + h) * kHeadDim + 8 * g;
+        const auto at = [](const float *base, int64_t first, unsigned lane_at, int i) {
+            return *reinterpret_cast<const f4 *>(reinterpret_cast<const char *>(base + first) + lane_at + 16 * i);
+        };
+        const int64_t mat = ph * (kHeadDim * kHeadDim) + 32 * slab * kHeadDim, row = ph * (kChunk * kHeadDim) + 32 * slab;
+        const unsigned mine = 32 * here(threadIdx.x), own = (tok * kHeadDim + 8 * g) * 4;
+        m0 = at(a.f.states, mat, mine, 0);
+        m1 = at(a.f.states, mat, mine, 1);
+        g0 = at(a.dstates, mat, mine, 0);
+        g1 = at(a.dstates, mat, mine, 1);
+        r0 = at(a.r, row, own, 0);
+        r1 = at(a.r, row, own, 1);
+        d0 = at(a.f.delta, row, own, 0);
+        d1 = at(a.f.delta, row, own, 1);
+        // d_out and v past the last token read zero
+        o = Rows<ET>(a.f.d_out, t0, n, h, Hv).load8(tok, 32 * slab + 8 * g);
+        v = Rows<ET>(a.f.v, t0, n, h, Hv).load8(tok, 32 * slab + 8 * g);
+    };
+    const auto load_head = [&](int h) {
+        const int64_t ph = static_cast<int64_t>(place) * Hv + h;
+        const float *pvec = reinterpret_cast<const float *>(a.f.within + (ph + 1) * within_bytes(3) - 1024);
+        if (threadIdx.x < kChunk) gx = a.gsum[ph * kChunk + threadIdx.x];
+        if (threadIdx.x < kVecFloats) vx = pvec[threadIdx.x];
+        odx = a.f.od[(ph * 8 + wave) * kChunk + lane];
+        if (threadIdx.x < 8) dux = a.du[ph * 8 + threadIdx.x];
+        load(h, 0);
+    };
+    load_head(kh);
+    load_planes<ET, NP, 512>(a.f, 0, lds, place, t0, n, kh);
+    if (kStays) load_planes<ET, NP, 512>(a.f, 1, lds + kQ, place, t0, n, kh);
+    f4 dq[4] = {}, dk[4] = {};                            // rows 16 w + 4 g + e, column dk 16 (4 p + t) + r
+#pragma unroll 1
+    for (int h = kh; h < Hv; h += Hk) {
+        // F or E between tiles of 16 tokens, lane: the own token, element: the other's;
+        // with the tiles up to the own as the earlier ones, P[t], and from the own on as the
+        // later ones, P[t + 1].
+        f4 P[5] = {}, om[4] = {}, rm[4] = {}, dg[4] = {}; // and d_out M, R M and Delta G
+        float dot = 0.0f, gm = 0.0f;
+#pragma unroll 1
         for (int slab = 0; slab < 4; ++slab) {
-            u4 rp[NO], dp[NO], op[NP] = {};
+            const int lane = here(threadIdx.x) & 63, r = lane & 15, g = lane >> 4, tok = w * 16 + r;
+            u4 op[NO] = {}, rp[NO], dp[NO];
+            wait_lds();
+            meet();                                       // the last slab, or F and E, is read
             {
-                const f4 r0 = *reinterpret_cast<const f4 *>(pr + 32 * slab), r1 = *reinterpret_cast<const f4 *>(pr + 32 * slab + 4);
-                const f4 d0 = *reinterpret_cast<const f4 *>(pd + 32 * slab), d1 = *reinterpret_cast<const f4 *>(pd + 32 * slab + 4);
+                const int mr = here(threadIdx.x) >> 4, mc = here(threadIdx.x) & 15;  // this thread's piece of M and G
+                u4 mp[NO], gp[NO];
+                planes_of<NO>(m0, m1, mp);
+                planes_of<NO>(g0, g1, gp);
                 planes_of<NO>(r0, r1, rp);
                 planes_of<NO>(d0, d1, dp);
-                if (tok < n) {
-                    load_planes<ET, NP>(a.f.d_out, vat + 32 * slab, op);
-                    const auto v = Pack<bits, 8>::load(static_cast<const bits *>(a.f.v) + vat + 32 * slab);
+                if constexpr (NP == 1)
+                    op[0] = o.x[0];
+                else
+                    planes_of<NO>(Rows<ET>::four(o, 0), Rows<ET>::four(o, 1), op);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        rd = fmaf(r0[e], d0[e], rd);
-                        rd = fmaf(r1[e], d1[e], rd);
-                        rv = fmaf(r0[e], ET::get(v[e]), rv);
-                        rv = fmaf(r1[e], ET::get(v[4 + e]), rv);
-                    }
+                for (int m = 0; m < NO; ++m) {
+                    *reinterpret_cast<u4 *>(lm + m * kMat + plane_at(mr, mc)) = mp[m];
+                    *reinterpret_cast<u4 *>(lg + m * kMat + plane_at(mr, mc)) = gp[m];
+                    *reinterpret_cast<u4 *>(lx + m * kTok + tok_at(tok, g)) = p == 0 ? op[m] : rp[m];
+                    if (p == 0) *reinterpret_cast<u4 *>(ld + m * kTok + tok_at(tok, g)) = dp[m];
                 }
-            }
-            if (slab > 0) __syncthreads();                // the last slab is read
-#pragma unroll
-            for (int p = 0; p < NO; ++p) {
-                *reinterpret_cast<u4 *>(lr + p * kTok + tok_at(tok, g)) = rp[p];
-                *reinterpret_cast<u4 *>(ld + p * kTok + tok_at(tok, g)) = dp[p];
-            }
-#pragma unroll
-            for (int p = 0; p < NP; ++p) *reinterpret_cast<u4 *>(lo + p * kTok + tok_at(tok, g)) = op[p];
-            // M and G: 32 rows of 16 chunks of eight
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int at = i * 256 + threadIdx.x, rr = at >> 4, ch = at & 15;
-                const int64_t src = ph * (kHeadDim * kHeadDim) + (32 * slab + rr) * kHeadDim + 8 * ch;
-                const f4 m0 = *reinterpret_cast<const f4 *>(a.f.states + src), m1 = *reinterpret_cast<const f4 *>(a.f.states + src + 4);
-                const f4 g0 = *reinterpret_cast<const f4 *>(a.dstates + src), g1 = *reinterpret_cast<const f4 *>(a.dstates + src + 4);
+                const f4 v0 = Rows<ET>::four(v, 0), v1 = Rows<ET>::four(v, 1);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     gm = fmaf(m0[e], g0[e], gm);
                     gm = fmaf(m1[e], g1[e], gm);
+                    dot = fmaf(r0[e], p == 0 ? v0[e] : d0[e], dot);
+                    dot = fmaf(r1[e], p == 0 ? v1[e] : d1[e], dot);
                 }
-                u4 mp[NO], gp[NO];
-                planes_of<NO>(m0, m1, mp);
-                planes_of<NO>(g0, g1, gp);
-#pragma unroll
-                for (int p = 0; p < NO; ++p) {
-                    *reinterpret_cast<u4 *>(lm + p * kMat + plane_at(rr, ch)) = mp[p];
-                    *reinterpret_cast<u4 *>(lg + p * kMat + plane_at(rr, ch)) = gp[p];
+                if (slab == 1) {                          // (the last head is done with them)
+                    if (threadIdx.x < kChunk) gs[threadIdx.x] = gx;
+                    if (threadIdx.x < kVecFloats) vec[threadIdx.x] = vx;
+                    ods[wave][lane] = odx;
+                    if (threadIdx.x < 8) dus[threadIdx.x] = dux;
                 }
             }
-            __syncthreads();
+            if (slab < 3)
+                load(h, slab + 1);
+            else if (h + Hk < Hv)
+                load_head(h + Hk);
+            wait_lds();
+            meet();                                       // (the loads stay on their way)
+#pragma unroll
+            for (int u = 0; u < 5; ++u) {
+                const bool to = u <= w;
+                const char *other = to ? ld : lx;
+                u4 oj[NO], ow[NO];
+#pragma unroll
+                for (int m = 0; m < NO; ++m) {
+                    oj[m] = *reinterpret_cast<const u4 *>(other + m * kTok + tok_at((to ? u : u - 1) * 16 + r, g));
+                    ow[m] = to ? (p == 0 ? op[m] : rp[m]) : dp[m];
+                }
+                P[u] = mma_planes<NO - 1>(oj, ow, P[u]);
+            }
+            // rows 8 g + e of the slab are an operand's k
+            const int column = here(slab_place(r, g));
+            u4 on[NP];
+#pragma unroll
+            for (int m = 0; m < NP; ++m) on[m] = op[m];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                u4 rj[NO], dj[NO], oj[NP];
+                u4 mcol[NO], gcol[NO];
 #pragma unroll
-                for (int p = 0; p < NO; ++p) {
-                    rj[p] = *reinterpret_cast<const u4 *>(lr + p * kTok + tok_at(t * 16 + r, g));
-                    dj[p] = *reinterpret_cast<const u4 *>(ld + p * kTok + tok_at(t * 16 + r, g));
+                for (int m = 0; m < NO; ++m) {
+                    mcol[m] = slab_columns(lm + m * kMat, 4 * p + t, column);
+                    gcol[m] = slab_columns(lg + m * kMat, 4 * p + t, column);
                 }
-#pragma unroll
-                for (int p = 0; p < NP; ++p) oj[p] = *reinterpret_cast<const u4 *>(lo + p * kTok + tok_at(t * 16 + r, g));
-                if (t <= wave) {
-                    F1[t] = mma_planes<NO - 1>(dj, op, F1[t]);
-                    E1[t] = mma_planes<NO - 1>(dj, rp, E1[t]);
-                }
-                if (t >= wave) {
-                    F2[t] = mma_planes<NO - 1>(oj, dp, F2[t]);
-                    E2[t] = mma_planes<NO - 1>(rj, dp, E2[t]);
-                }
-            }
-            // rows 8 g + e of the slab are an operand's k; column dk 16 t + r
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                u4 mc[NO], gc[NO];
-#pragma unroll
-                for (int p = 0; p < NO; ++p) {
-                    mc[p] = slab_columns(lm + p * kMat, t, r, g);
-                    gc[p] = slab_columns(lg + p * kMat, t, r, g);
-                }
-                Z[t] = mma_planes<NO - 1>(op, mc, Z[t]);
-                Wm[t] = mma_planes<NO - 1>(rp, mc, Wm[t]);
-                H[t] = mma_planes<NO - 1>(dp, gc, H[t]);
+                om[t] = mma_planes<NO - 1>(on, mcol, om[t]);
+                rm[t] = mma_planes<NO - 1>(rp, mcol, rm[t]);
+                dg[t] = mma_planes<NO - 1>(dp, gcol, dg[t]);
             }
         }
-        __syncthreads();                                  // the slabs are read: K and Q take their place
-        load_kq<ET, NP>(a.f, lds, place, t0, n, kh);
-        // decays and masks; F1 and E1 are j <= i = tok, F2 and E2 i >= j = tok
-        const double gt = gs[tok];
-        const float bt = vec[2 * kChunk + tok];
+        const int lane = here(threadIdx.x) & 63, r = lane & 15, g = lane >> 4, tok = w * 16 + r;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int e = 0; e < 4; ++e) {
+            const int row = w * 16 + 4 * g + e;
+            const float rise = vec[row], fall = vec[kChunk + row], beta = vec[2 * kChunk + row];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int o = t * 16 + 4 * g + e;
-                float e1 = 0.0f, e2 = 0.0f, f1 = 0.0f, f2 = 0.0f;
-                if (o <= tok) {
-                    const float d = expf(static_cast<float>(gt - gs[o]));
-                    f1 = kReadScale * (d * F1[t][e]);
-                    e1 = o < tok ? -bt * (d * E1[t][e]) : 0.0f;
-                }
-                if (o >= tok) {
-                    const float d = expf(static_cast<float>(gs[o] - gt));
-                    f2 = kReadScale * (d * F2[t][e]);
-                    e2 = o > tok ? -vec[2 * kChunk + o] * (d * E2[t][e]) : 0.0f;
-                }
-                F1[t][e] = f1;
-                F2[t][e] = f2;
-                E1[t][e] = e1 + e2;
+            for (int t = 0; t < 4; ++t) {
+                dq[t][e] = fmaf(kReadScale * rise, om[t][e], dq[t][e]);
+                dk[t][e] = fmaf(fall, dg[t][e], fmaf(-beta * rise, rm[t][e], dk[t][e]));
             }
+        }
+        wait_lds();
+        meet();                                           // the slabs are read: F and E take their place
+        if (!kStays) load_planes<ET, NP, 512>(a.f, 1, lds + kQ, place, t0, n, kh);
+        // decays and masks
+        const double gt = gs[tok];
+        if (p == 0) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                f4 early[2], late[2];
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int i = (2 * half + t) * 16 + 4 * g + e;
+                        const double x = gt - gs[i];
+                        const float d = kReadScale * decay(i <= tok ? x : -x);
+                        early[t][e] = i <= tok ? d * P[2 * half + t][e] : 0.0f;
+                        late[t][e] = i >= tok ? d * P[2 * half + t + 1][e] : 0.0f;
+                    }
+                u4 f[NO];
+                if (2 * half <= w) {
+                    planes_of<NO>(early[0], early[1], f);
+#pragma unroll
+                    for (int m = 0; m < NO; ++m) *reinterpret_cast<u4 *>(pass_at(lane, 0, half, m)) = f[m];
+                }
+                if (2 * half + 1 >= w) {
+                    planes_of<NO>(late[0], late[1], f);
+#pragma unroll
+                    for (int m = 0; m < NO; ++m) *reinterpret_cast<u4 *>(pass_at(lane, 1, half, m)) = f[m];
+                }
+            }
+        } else {
+            const float beta = vec[2 * kChunk + tok];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                f4 both[2];                               // E + E^T
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int i = (2 * half + t) * 16 + 4 * g + e;
+                        const double x = gt - gs[i];
+                        const float d = decay(i < tok ? x : -x);
+                        const float y = i < tok ? beta * P[2 * half + t][e] : vec[2 * kChunk + i] * P[2 * half + t + 1][e];
+                        both[t][e] = i == tok ? 0.0f : -d * y;
+                    }
+                u4 f[NO];
+                planes_of<NO>(both[0], both[1], f);
+#pragma unroll
+                for (int m = 0; m < NO; ++m) *reinterpret_cast<u4 *>(pass_at(lane, 2, half, m)) = f[m];
+            }
+        }
         // per token: the sums over dv of its four lanes
-        rd += __shfl_xor(rd, 16);
-        rd += __shfl_xor(rd, 32);
-        rv += __shfl_xor(rv, 16);
-        rv += __shfl_xor(rv, 32);
+        dot += __shfl_xor(dot, 16);
+        dot += __shfl_xor(dot, 32);
         double gd = gm;
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) gd += __shfl_xor(gd, d);
-        if (g == 0) {
-            dots[0][tok] = rd;
-            dots[1][tok] = rv;
-        }
+        if (g == 0) dots[p][tok] = dot;
         if (lane == 0) part[wave] = gd;
-        __syncthreads();
+        wait_lds();
+        meet();
         if (wave == 0) {
-            const float beta = vec[2 * kChunk + lane];
-            double od = 0.0, du = lane < 8 ? a.du[ph * 8 + lane] : 0.0f;
+            const float bl = vec[2 * kChunk + lane];
+            double od = 0.0, du = 0.0, mg = 0.0;
 #pragma unroll
-            for (int w = 0; w < 8; ++w) od += a.f.od[(ph * 8 + w) * kChunk + lane];
+            for (int i = 0; i < 8; ++i) od += ods[i][lane];
 #pragma unroll
-            for (int d = 1; d < 8; d *= 2) du += __shfl_xor(du, d);
-            const double end = lane_of(du, 0) + static_cast<double>(vec[kChunk - 1]) * (part[0] + part[1] + part[2] + part[3]);
-            double x = od - static_cast<double>(fabsf(beta) <= kLeastBeta ? 0.0f : beta) * dots[1][lane];
+            for (int i = 0; i < 8; ++i) mg += part[i];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) du += dus[i];
+            const double end = du + static_cast<double>(vec[kChunk - 1]) * mg;
+            double y = od - static_cast<double>(fabsf(bl) <= kLeastBeta ? 0.0f : bl) * dots[0][lane];
 #pragma unroll
             for (int d = 1; d < 64; d *= 2) {
-                const double y = __shfl_down(x, d);
-                if (lane + d < 64) x += y;
+                const double z = __shfl_down(y, d);
+                if (lane + d < 64) y += z;
             }
             if (lane < n) {
-                a.dgate[(t0 + lane) * Hv + h] = static_cast<float>(x + end);
-                a.dbeta[(t0 + lane) * Hv + h] = dots[0][lane] / beta;
+                a.dgate[(t0 + lane) * Hv + h] = static_cast<float>(y + end);
+                a.dbeta[(t0 + lane) * Hv + h] = dots[1][lane] / bl;
             }
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = wave * 16 + 4 * g + e;
-            const float rise = vec[i], fall = vec[kChunk + i], beta = vec[2 * kChunk + i];
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                dq[t][e] = fmaf(kReadScale * rise, Z[t][e], dq[t][e]);
-                dk[t][e] = fmaf(-beta * rise, Wm[t][e], fmaf(fall, H[t][e], dk[t][e]));
-            }
-        }
+        const int column = here(plain_place(r, g));
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            u4 f1[NO], f2[NO], e1[NO];
-            planes_of<NO>(F1[2 * half], F1[2 * half + 1], f1);
-            planes_of<NO>(F2[2 * half], F2[2 * half + 1], f2);
-            planes_of<NO>(E1[2 * half], E1[2 * half + 1], e1);
+            u4 f[NO], e[NO];
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                u4 kc[NP], qc[NP];
+            for (int m = 0; m < NO; ++m) {
+                f[m] = *reinterpret_cast<const u4 *>(pass_at(lane, 0, half, m));
+                e[m] = *reinterpret_cast<const u4 *>(pass_at(lane, 2, half, m));
+            }
 #pragma unroll
-                for (int p = 0; p < NP; ++p) {
-                    kc[p] = plain_columns(lds + p * kPlaneBytes, half, t, r, g);
-                    qc[p] = plain_columns(lds + (NP + p) * kPlaneBytes, half, t, r, g);
-                }
-                dq[t] = mma_planes<NO - 1>(f1, kc, dq[t]);
-                dk[t] = mma_planes<NO - 1>(f2, qc, dk[t]);
-                dk[t] = mma_planes<NO - 1>(e1, kc, dk[t]);
+            for (int t = 0; t < 4; ++t) {
+                u4 kc[NP];
+#pragma unroll
+                for (int m = 0; m < NP; ++m) kc[m] = plain_columns(lds + m * kPlaneBytes, half, 4 * p + t, column);
+                if (2 * half <= w) dq[t] = mma_planes<NO - 1>(f, kc, dq[t]);
+                dk[t] = mma_planes<NO - 1>(e, kc, dk[t]);
             }
         }
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+            if (2 * half + 1 >= w) {
+                u4 f[NO];
+#pragma unroll
+                for (int m = 0; m < NO; ++m) f[m] = *reinterpret_cast<const u4 *>(pass_at(lane, 1, half, m));
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    u4 qc[NP];
+#pragma unroll
+                    for (int m = 0; m < NP; ++m) qc[m] = plain_columns(lds + kQ + m * kPlaneBytes, half, 4 * p + t, column);
+                    dk[t] = mma_planes<NO - 1>(f, qc, dk[t]);
+                }
+            }
     }
-    bits *qo = static_cast<bits *>(a.dq), *ko = static_cast<bits *>(a.dk);
+    const Rows<ET> qo(a.dq, t0, n, kh, Hk), ko(a.dk, t0, n, kh, Hk);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int i = wave * 16 + 4 * g + e;
-        if (i >= n) continue;
-        const int64_t at = ((t0 + i) * Hk + kh) * kHeadDim + r;
+    for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            qo[at + 16 * t] = ET::put(dq[t][e]);
-            ko[at + 16 * t] = ET::put(dk[t][e]);
+        for (int t = 0; t < 4; ++t) {
+            qo.store(w * 16 + 4 * g + e, 16 * (4 * p + t) + r, dq[t][e]);
+            ko.store(w * 16 + 4 * g + e, 16 * (4 * p + t) + r, dk[t][e]);
         }
-    }
 }
 
 // Waves a workgroup as in launch_walk.
@@ -529,7 +604,7 @@ hipError_t launch(const BackArgs &a, hipStream_t s) {
     e = launch_back<ET, NP, S>(a, s);
     if (e != hipSuccess) return e;
     const int64_t places = chunk_places(a.f.s.B, a.f.s.tokens) * a.f.s.Hk;
-    k_grad<ET, NP, NO><<<dim3(static_cast<unsigned>(places)), dim3(256), 0, s>>>(a);
+    k_grad<ET, NP, NO><<<dim3(static_cast<unsigned>(places)), dim3(512), 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -112,6 +112,12 @@ __device__ __forceinline__ void wait_all() {
     __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));
     asm volatile("" ::: "memory");
 }
+// None of this wave's LDS operations is still on its way.
+__device__ __forceinline__ void wait_lds() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    asm volatile("" ::: "memory");
+}
 __device__ __forceinline__ void meet() {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
@@ -146,6 +152,24 @@ struct Rows {
             return f4{ET::get(v[0]), ET::get(v[1]), ET::get(v[2]), ET::get(v[3])};
         } else {
             return __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(rows, token * stride + at * kBytes, 0, 0));
+        }
+    }
+    // eight elements as they are in memory, and their values
+    struct Eight { u4 x[kBytes / 2]; };
+    __device__ __forceinline__ Eight load8(int token, int at) const {
+        Eight v;
+#pragma unroll
+        for (int i = 0; i < kBytes / 2; ++i)
+            v.x[i] = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(rows, token * stride + at * kBytes + 16 * i, 0, 0));
+        return v;
+    }
+    static __device__ __forceinline__ f4 four(const Eight &v, int i) {
+        if constexpr (kBytes == 2) {
+            typedef bits b8 __attribute__((ext_vector_type(8)));
+            const b8 y = __builtin_bit_cast(b8, v.x[0]);
+            return f4{ET::get(y[4 * i]), ET::get(y[4 * i + 1]), ET::get(y[4 * i + 2]), ET::get(y[4 * i + 3])};
+        } else {
+            return __builtin_bit_cast(f4, v.x[i]);
         }
     }
     __device__ __forceinline__ void store(int token, int at, float x) const {
