@@ -5,16 +5,25 @@
 // T = sum exp(x - m) (x - m):
 //   log p(v) = x_v - m - log Z,   H = log Z - T / Z.
 // A thread keeps its own m and rescales Z and T when it grows; threads are joined
-// in binary64, so that log p of a nearly certain token keeps its digits.
+// in binary64, so that log p of a nearly certain token keeps its digits.  In
+// powers of two, with c the binary32 number next to log2 e: each term is
+// 2^(c x - R), one fma and one exponential, where R is c m rounded to binary32 (or
+// c m itself where m is so large that c x would overflow).  For that the
+// reference is R / c in place of m; and as c log 2 = 1 - e, e = 1.3e-8, log Z lacks
+// e times the mean of x - R / c, which T gives.
 //
-// The most likely tokens need no work per entry: the K-th largest of the
-// groups' own maxima (a group: the entries of four neighbouring threads) bounds
-// the K-th largest entry from below, only the groups that reach it are read
+// The most likely tokens need no work per entry: the K-th largest of the maxima of
+// groups (the entries of four neighbouring threads) bounds the K-th largest entry
+// from below, only the entries of threads whose own maximum reaches it are read
 // again (from the caches), and what passes is ranked.  Orders by value, then by
 // the lower id: a 64-bit key of both.
 //
-// One pass over memory, a row in as many units as fill the chip; a second launch
-// joins the units where there are several.
+// One pass over memory, a row in as many units as give every compute unit four; a
+// second launch joins the units where there are several.  The exponentials and their
+// sums bound it, eight instructions an entry of which one takes four times as
+// long: 1024 rows x 131071 bf16 66 us (4.0 TB/s), the best 20 with them 85 (two units a
+// row and their join: 75 and 94); 32 x 128000 with 20 16 us; the next vectors on
+// their way during the sums: no gain.
 #include "gdn.h"
 #include "gdn_elem.hpp"
 #include "gdn_launch.hpp"
@@ -28,6 +37,8 @@ constexpr int kGroups = kT / 4;
 constexpr int kAhead = 4;                    // vectors that a thread fetches at once
 constexpr int kList = 512;                   // entries that are ranked at most
 constexpr float kLog2e = 1.44269504088896f;
+constexpr double kLn2 = 0.693147180559945309417, kLacks = 1.0 - kLn2 * kLog2e;
+constexpr float kLarge = 0x1p100f;
 constexpr float kLeast = -3.402823466e38f;
 
 // Orders as the values, -0 as 0; 0 is below every float's.
@@ -45,24 +56,31 @@ __device__ __forceinline__ uint64_t key_of(float x, int id) {
 __device__ __forceinline__ int id_of(uint64_t key) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(key)); }
 constexpr uint64_t kNone = 0;                // below every entry's key
 
-// Sums of entries relative to m.
+// R of m.
+__device__ __forceinline__ double reference(float m) {
+    return fabsf(m) < kLarge ? static_cast<double>(m * kLog2e) : static_cast<double>(m) * kLog2e;
+}
+// Sums of the entries' 2^(c x - R) and of these times c x - R.
 struct Sums {
     float m;
     double z, t;
 };
-// a joined with b; of NaNs, NaN.
-__device__ __forceinline__ Sums join(const Sums &a, const Sums &b) {
+// L lanes' sums joined in each of them; of NaNs, NaN.
+template <int L>
+__device__ __forceinline__ Sums joined(const Sums &s) {
     Sums c;
-    c.m = fmaxf(a.m, b.m);
-    const double da = static_cast<double>(a.m) - c.m, db = static_cast<double>(b.m) - c.m;
-    const double ea = exp(da), eb = exp(db);
-    c.z = a.z * ea + b.z * eb;
-    // the weight of what is far below is 0, whatever its distance
-    c.t = (ea > 0.0 ? ea * (a.t + da * a.z) : a.z * 0.0) + (eb > 0.0 ? eb * (b.t + db * b.z) : b.z * 0.0);
+    c.m = s.m;
+#pragma unroll
+    for (int d = 1; d < L; d *= 2) c.m = fmaxf(c.m, __shfl_xor(c.m, d));
+    const double d = reference(s.m) - reference(c.m), e = exp2(d);
+    c.z = s.z * e;
+    c.t = e > 0.0 ? e * (s.t + d * s.z) : s.z * 0.0;      // what is far below counts 0, whatever its distance
+#pragma unroll
+    for (int d = 1; d < L; d *= 2) {
+        c.z += __shfl_xor(c.z, d);
+        c.t += __shfl_xor(c.t, d);
+    }
     return c;
-}
-__device__ __forceinline__ Sums from_lane(const Sums &s, int d) {
-    return Sums{__shfl_xor(s.m, d), __shfl_xor(s.z, d), __shfl_xor(s.t, d)};
 }
 
 // Entries v.. of a row, N of them; those past its end or before v are -inf.
@@ -87,14 +105,14 @@ __device__ __forceinline__ void answer(const LogprobsArgs &a, int64_t row, const
     const typename LT::bits *x = static_cast<const typename LT::bits *>(a.logits) + row * a.ld;
     const bool bad = !(s.z >= 0.0) || s.m == __builtin_inff();       // a NaN or +inf
     const bool none = s.z == 0.0;                                    // nothing above -inf
-    const double lz = log(s.z);
+    const double ref = reference(s.m) / kLog2e, mean = s.t / s.z / kLog2e, lz = log(s.z) + kLacks * mean;
     const auto logprob = [&](float v) {
         // m first: a row of the type's lowest value is uniform
         return bad ? __builtin_nanf("")
-                   : none ? -__builtin_inff() : static_cast<float>((static_cast<double>(v) - s.m) - lz);
+                   : none ? -__builtin_inff() : static_cast<float>((static_cast<double>(v) - ref) - lz);
     };
     if (lane == 0) {
-        if (a.entropy) a.entropy[row] = bad ? __builtin_nanf("") : none ? 0.0f : static_cast<float>(lz - s.t / s.z);
+        if (a.entropy) a.entropy[row] = bad ? __builtin_nanf("") : none ? 0.0f : static_cast<float>(lz - mean);
         if (a.tokens) {
             const int t = a.tokens[row];
             a.logprob[row] = t >= 0 && t < a.V ? logprob(LT::get(x[t])) : bad ? __builtin_nanf("") : -__builtin_inff();
@@ -129,8 +147,8 @@ __global__ __launch_bounds__(kT) void k_logprobs(LogprobsArgs a, int unit, int u
     __shared__ Sums sums[kT / 64];
     __shared__ alignas(16) uint32_t tops[kGroups];
     __shared__ uint64_t list[kList], best[kLogprobsMaxTop];
-    __shared__ int groups[kGroups];
-    __shared__ int n_groups, n_list;
+    __shared__ int threads[kT];
+    __shared__ int n_threads, n_list;
     __shared__ uint32_t bound_s;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t row = kOne ? blockIdx.x : blockIdx.x / units;
@@ -141,21 +159,28 @@ __global__ __launch_bounds__(kT) void k_logprobs(LogprobsArgs a, int unit, int u
     const int turns = static_cast<int>((end - v0 + kT * N - 1) / (kT * N));   // vectors of a thread
 
     float m = kLeast, z = 0.0f, t = 0.0f;
-    const auto add = [&](const float (&y)[N]) {
-        float top = y[0];
-#pragma unroll
-        for (int j = 1; j < N; ++j) top = fmaxf(top, y[j]);
+    // the batch's largest, then its entries by get(j)
+    const auto add = [&](float top, int n, auto get) {
         if (top > m) {
-            const float d = m - top, e = __builtin_amdgcn_exp2f(d * kLog2e);
+            const float d = static_cast<float>(reference(m) - reference(top)), e = __builtin_amdgcn_exp2f(d);
             t = e > 0.0f ? e * fmaf(d, z, t) : z * 0.0f;
             z *= e;
             m = top;
         }
+        if (fabsf(m) < kLarge) {
+            const float r = m * kLog2e;
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const float d = y[j] - m, e = __builtin_amdgcn_exp2f(d * kLog2e);
-            z += e;
-            t = fmaf(e, fmaxf(d, -200.0f), t);            // of -inf: 0
+            for (int j = 0; j < n; ++j) {
+                const float d = fmaf(get(j), kLog2e, -r), e = __builtin_amdgcn_exp2f(d);
+                z += e;
+                t = fmaf(e, fmaxf(d, -300.0f), t);        // of -inf: 0
+            }
+        } else {
+            for (int j = 0; j < n; ++j) {
+                const float d = (get(j) - m) * kLog2e, e = __builtin_amdgcn_exp2f(d);
+                z += e;
+                t = fmaf(e, fmaxf(d, -300.0f), t);
+            }
         }
     };
     int i = 0;
@@ -163,30 +188,30 @@ __global__ __launch_bounds__(kT) void k_logprobs(LogprobsArgs a, int unit, int u
         typename Pack<bits, N>::vec w[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) w[k] = Pack<bits, N>::load(x + v0 + (static_cast<int64_t>(i + k) * kT + tid) * N);
+        float top = LT::get(w[0][0]);
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            float y[N];
+        for (int k = 0; k < kAhead; ++k)
 #pragma unroll
-            for (int j = 0; j < N; ++j) y[j] = LT::get(w[k][j]);
-            add(y);
-        }
+            for (int j = 0; j < N; ++j) top = fmaxf(top, LT::get(w[k][j]));
+        add(top, kAhead * N, [&](int j) { return LT::get(w[j / N][j % N]); });
     }
     for (; i < turns; ++i) {
         float y[N];
         load<LT, N>(x, v0 + (static_cast<int64_t>(i) * kT + tid) * N, end, y);
-        add(y);
+        float top = y[0];
+#pragma unroll
+        for (int j = 1; j < N; ++j) top = fmaxf(top, y[j]);
+        add(top, N, [&](int j) { return y[j]; });
     }
     // groups' maxima; the best `top` entries
     if (a.top > 0) {
         float gm = fmaxf(m, __shfl_xor(m, 1));
         gm = fmaxf(gm, __shfl_xor(gm, 2));
         if ((tid & 3) == 0) tops[tid >> 2] = order(gm);
-        if (tid == 0) n_groups = n_list = 0;
+        if (tid == 0) n_threads = n_list = 0;
         if (tid < kLogprobsMaxTop) best[tid] = kNone;
     }
-    Sums s{m, z, t};
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) s = join(s, from_lane(s, d));
+    Sums s = joined<64>(Sums{m, z, t});
     if (lane == 0) sums[wave] = s;
     __syncthreads();
     if (a.top > 0) {
@@ -201,27 +226,21 @@ __global__ __launch_bounds__(kT) void k_logprobs(LogprobsArgs a, int unit, int u
         }
         __syncthreads();
         const uint32_t bound = bound_s;
-        if (wave == 0) {
-            const bool in = tops[lane] >= bound;
-            const unsigned long long b = __ballot(in);
-            if (in) groups[__popcll(b & ((1ull << lane) - 1))] = lane;
-            if (lane == 0) n_groups = __popcll(b);
-        }
+        if (order(m) >= bound) threads[atomicAdd(&n_threads, 1)] = tid;
         __syncthreads();
-        // a wave per listed group, a lane per vector of its threads
-        for (int k = wave; k < n_groups; k += kT / 64) {
-            const int g4 = groups[k] * 4;
-            for (int w = lane; w < turns * 4; w += 64) {
-                const int64_t v = v0 + (static_cast<int64_t>(w >> 2) * kT + g4 + (w & 3)) * N;
-                float y[N];
-                load<LT, N>(x, v, end, y);
+        // the listed threads' vectors, neighbouring threads' side by side
+        const int listed = n_threads;
+        for (int w = tid; w < listed * turns; w += kT) {
+            const int turn = w / listed;
+            const int64_t v = v0 + (static_cast<int64_t>(turn) * kT + threads[w - turn * listed]) * N;
+            float y[N];
+            load<LT, N>(x, v, end, y);
 #pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if (y[j] >= kLeast && order(y[j]) >= bound) {
-                        const int at = atomicAdd(&n_list, 1);
-                        if (at < kList) list[at] = key_of(y[j], static_cast<int>(v + j));
-                    }
-            }
+            for (int j = 0; j < N; ++j)
+                if (y[j] >= kLeast && order(y[j]) >= bound) {
+                    const int at = atomicAdd(&n_list, 1);
+                    if (at < kList) list[at] = key_of(y[j], static_cast<int>(v + j));
+                }
         }
         __syncthreads();
         const int n = n_list;
@@ -264,9 +283,7 @@ __global__ __launch_bounds__(kT) void k_logprobs(LogprobsArgs a, int unit, int u
         __syncthreads();
     }
     if (wave > 0) return;
-    s = sums[0];
-#pragma unroll
-    for (int w = 1; w < kT / 64; ++w) s = join(s, sums[w]);
+    s = joined<kT / 64>(sums[lane % (kT / 64)]);
     if constexpr (kOne) {
         answer<LT>(a, row, s, best);
     } else {
@@ -280,33 +297,52 @@ __global__ __launch_bounds__(kT) void k_logprobs(LogprobsArgs a, int unit, int u
     }
 }
 
-// The units of a row joined by one wave, a unit a lane.
+// The units of a row joined: the sums by the first wave, and each unit's keys, which
+// are in order: those that reach a bound, which `top` of them do, are ranked.
 template <typename LT>
-__global__ __launch_bounds__(64) void k_join(LogprobsArgs a, int units) {
-    __shared__ uint64_t best[kLogprobsMaxTop];
-    const int lane = threadIdx.x;
+__global__ __launch_bounds__(kT) void k_join(LogprobsArgs a, int units) {
+    constexpr int kKeys = kLogprobsMaxUnits * kLogprobsMaxTop;
+    __shared__ uint64_t keys[kKeys], list[kKeys], best[kLogprobsMaxTop], bound;
+    __shared__ int n_list;
+    const int tid = threadIdx.x;
     const int64_t row = blockIdx.x;
     Sums s{kLeast, 0.0, 0.0};
-    const int64_t at = row * units + lane;
-    if (lane < units) s = Sums{static_cast<float>(a.sums[at * 3]), a.sums[at * 3 + 1], a.sums[at * 3 + 2]};
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) s = join(s, from_lane(s, d));
-    int next = 0;                                         // of this lane's unit
-    uint64_t head = lane < units && a.top > 0 ? a.keys[at * a.top] : kNone;
-    for (int k = 0; k < a.top; ++k) {
-        uint64_t key = head;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const uint64_t o = __shfl_xor(static_cast<unsigned long long>(key), d);
-            key = o > key ? o : key;
-        }
-        if (lane == 0) best[k] = key;
-        if (key != kNone && head == key) {
-            ++next;
-            head = next < a.top ? a.keys[at * a.top + next] : kNone;
-        }
+    if (tid < units) {
+        const double *from = a.sums + (row * units + tid) * 3;
+        s = Sums{static_cast<float>(from[0]), from[1], from[2]};
     }
-    __syncthreads();
+    if (a.top > 0) {
+        const int all = units * a.top;
+        for (int i = tid; i < all; i += kT) keys[i] = a.keys[row * all + i];
+        if (tid < kLogprobsMaxTop) best[tid] = kNone;
+        if (tid == 0) n_list = 0;
+        __syncthreads();
+        // `of` units have `each` keys at or above the bound, `top` together
+        const int each = min(a.top, (2 * a.top + units - 1) / units), of = (a.top + each - 1) / each;
+        if (tid < units) {
+            const uint64_t mine = keys[tid * a.top + each - 1];
+            int above = 0;
+            for (int u = 0; u < units; ++u) {
+                const uint64_t key = keys[u * a.top + each - 1];
+                above += key > mine || (key == mine && u < tid);
+            }
+            if (above == of - 1) bound = mine;
+        }
+        __syncthreads();
+        for (int i = tid; i < all; i += kT)
+            if (keys[i] != kNone && keys[i] >= bound) list[atomicAdd(&n_list, 1)] = keys[i];
+        __syncthreads();
+        const int n = n_list;
+        for (int i = tid; i < n; i += kT) {
+            const uint64_t key = list[i];
+            int rank = 0;
+            for (int j = 0; j < n; ++j) rank += list[j] > key;
+            if (rank < a.top) best[rank] = key;
+        }
+        __syncthreads();
+    }
+    if (tid >= 64) return;
+    s = joined<64>(s);
     answer<LT>(a, row, s, best);
 }
 
@@ -321,7 +357,7 @@ hipError_t launch(const LogprobsArgs &a, int64_t units, hipStream_t s) {
         <<<dim3(static_cast<unsigned>(a.rows * units)), dim3(kT), 0, s>>>(a, unit, static_cast<int>(units));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    k_join<LT><<<dim3(static_cast<unsigned>(a.rows)), dim3(64), 0, s>>>(a, static_cast<int>(units));
+    k_join<LT><<<dim3(static_cast<unsigned>(a.rows)), dim3(kT), 0, s>>>(a, static_cast<int>(units));
     return hipGetLastError();
 }
 

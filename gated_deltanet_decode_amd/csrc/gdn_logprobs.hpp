@@ -28,7 +28,7 @@ constexpr int kLogprobsMaxUnits = 64;
 
 // Units that a row is read in, a workgroup each.
 constexpr int64_t logprobs_units(int64_t rows, int64_t V) {
-    const int64_t fill = (2048 + rows - 1) / rows, most = (V + 4095) / 4096;
+    const int64_t fill = (1024 + rows - 1) / rows, most = (V + 4095) / 4096;
     const int64_t n = fill < most ? fill : most;
     return n < kLogprobsMaxUnits ? n : kLogprobsMaxUnits;
 }
