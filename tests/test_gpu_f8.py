@@ -87,6 +87,21 @@ def test_code_borders(g, tall):
             check(g, r[None].cuda(), tall)
 
 
+@pytest.mark.parametrize("dtype,bits", [(torch.bfloat16, 8), (torch.float16, 11)], ids=["bf16", "f16"])
+def test_code_borders_16_bit(g, dtype, bits):
+    """Every value of ten binades under a block's largest magnitude, which runs through
+    its mantissas (64 of them for float16): each tie and what lies next to one."""
+    half = 2 ** (bits - 1)
+    mantissas = torch.arange(half, 2 * half, dtype=torch.float64)
+    tops = mantissas if bits == 8 else mantissas[torch.randperm(half, generator=torch.Generator().manual_seed(1))[:64]]
+    x = torch.cat([mantissas * 2.0**-s for s in range(1, 12)])
+    x = torch.cat([x, x.new_zeros(-len(x) % (B - 1))]).view(1, -1, B - 1).repeat(len(tops), 1, 1)
+    x[:, :, 1::2] *= -1
+    x = torch.cat([tops.view(-1, 1, 1).expand(-1, x.shape[1], 1), x], 2).reshape(len(tops), -1) * 16
+    assert torch.equal(x.to(dtype).double(), x)
+    check(g, x.to(dtype).cuda(), 1)
+
+
 @pytest.mark.parametrize("tall", [1, B])
 def test_codes_not_finite(g, tall):
     x = torch.randn(260, 400, generator=torch.Generator().manual_seed(1)).cuda()
