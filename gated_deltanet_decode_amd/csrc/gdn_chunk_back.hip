@@ -577,12 +577,8 @@ hipError_t launch_back_of(const BackArgs &a, hipStream_t s) {
 }
 template <typename ET, int NP, int S>
 hipError_t launch_back(const BackArgs &a, hipStream_t s) {
-    const int64_t heads = static_cast<int64_t>(a.f.s.B) * a.f.s.Hv;
-    const int cus = device_cus();
-    if (heads * 8 <= cus) return launch_back_of<ET, NP, 1, S>(a, s);
-    if (heads * 4 <= cus) return launch_back_of<ET, NP, 2, S>(a, s);
-    if (heads * 2 <= cus) return launch_back_of<ET, NP, 4, S>(a, s);
-    return launch_back_of<ET, NP, 8, S>(a, s);
+    const bool halves = halves_heads(static_cast<int64_t>(a.f.s.B) * a.f.s.Hv, device_cus());
+    return halves ? launch_back_of<ET, NP, 4, S>(a, s) : launch_back_of<ET, NP, 8, S>(a, s);
 }
 
 template <typename ET, int NP, int NO, int S>

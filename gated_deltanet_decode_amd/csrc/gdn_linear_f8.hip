@@ -698,20 +698,27 @@ hipError_t launch_tile(const LinearF8Args &a, int cus, hipStream_t s) {
 template <typename OT>
 hipError_t launch(const LinearF8Args &a, hipStream_t s) {
     const int cus = device_cus();
-    const auto fits = [&](int bn, int bm) {
-        return (bn <= 64 || bn < 2 * a.N) && (bm <= 16 || bm < 2 * a.M) &&
-               2 * tiles(a.N, bn) * tiles(a.M, bm) > static_cast<int64_t>(cus);
+    // The largest tile of which there are enough (and that is not mostly empty): half the
+    // compute units for those of 256 and 128, whose waves hide their own latency, more
+    // than that for the smaller ones.  Measured, in us, tile and next smaller one, bf16:
+    //   2048 x 4096 -> 4096 (128 tiles of 256): 59, 62;  1024 x 4096 -> 4096 (64): 56, 33
+    //   1024 x 2048 -> 2048 (128 of 128): 18.6, 21.7;     256 x 2048 -> 2048 (32): 16.5, 11.1
+    //   64 x 2048 -> 12352 (193 of 64 x 64): 12.9, 15.0;  256 x 2048 -> 2048 (128): 11.1, 7.7
+    //   32 x 2048 -> 12352 (193 of 64 x 32): 9.9, 12.7;   64 x 2048 -> 4096 (128): 7.3, 6.2
+    //   16 x 4096 -> 12288 (192 of 64 x 16): 11.8, 13.2;  1 x 4096 -> 4096 (64): 7.2, 5.0
+    // (64 x 128 and 32 x 64 were nowhere better than both neighbours by more than 5 %).
+    const auto fits = [&](int bn, int bm, int64_t least) {
+        return (bn <= 64 || bn < 2 * a.N) && (bm <= 16 || bm < 2 * a.M) && tiles(a.N, bn) * tiles(a.M, bm) >= least;
     };
+    const int64_t half = cus / 2;
     if constexpr (!__is_same(OT, F32))
-        if (fits(256, 256) && a.K % 256 == 0 && static_cast<int64_t>(a.M) * (a.K / kBK) < INT32_MAX)
+        if (fits(256, 256, half) && a.K % 256 == 0 && static_cast<int64_t>(a.M) * (a.K / kBK) < INT32_MAX)
             return launch_tile<OT>(a, cus, s);
-    if (fits(128, 128)) return launch_block<OT, 128, 128, 2, 4, 4>(a, s);
-    if (fits(64, 128)) return launch_block<OT, 64, 128, 2, 2, 4>(a, s);
-    if (fits(64, 64)) return launch_ring<OT, 4, 4, 4, 2>(a, s);
-    if (fits(32, 64)) return launch_ring<OT, 2, 4, 4, 3>(a, s);
-    if (fits(64, 32)) return launch_ring<OT, 4, 2, 4, 3>(a, s);
-    if (fits(32, 32)) return launch_ring<OT, 2, 2, 4, 4>(a, s);
-    if (fits(64, 16)) return launch_ring<OT, 4, 1, 4, 3>(a, s);
+    if (fits(128, 128, half)) return launch_block<OT, 128, 128, 2, 4, 4>(a, s);
+    if (fits(64, 64, half + 1)) return launch_ring<OT, 4, 4, 4, 2>(a, s);
+    if (fits(64, 32, half + 1)) return launch_ring<OT, 4, 2, 4, 3>(a, s);
+    if (fits(32, 32, half + 1)) return launch_ring<OT, 2, 2, 4, 4>(a, s);
+    if (fits(64, 16, half + 1)) return launch_ring<OT, 4, 1, 4, 3>(a, s);
     return launch_ring<OT, 1, 1, 8, 2>(a, s);
 }
 

@@ -291,8 +291,13 @@ __global__ __launch_bounds__(64 * W) void k_walk(ChunkArgs a, int parts) {
     }
 }
 
-// As many waves a workgroup (of 16 rows of a head's 128) as leave each compute unit
-// one: a wave alone on its SIMD goes through a chunk twice as fast as two of them.
+// Eight waves of 16 rows are a head; in two workgroups of four where that leaves each
+// compute unit one: a wave alone on its SIMD goes through a chunk faster than two of
+// them (2048 tokens, 32 heads a sequence, the whole of gdn_chunk, in two against one: 1
+// sequence 138 against 175 us, 3 168 against 200, 4 191 against 214, 6 343 against
+// 254; in four or eight never faster than in two by more than 1 %).
+constexpr bool halves_heads(int64_t heads, int cus) { return 2 * heads <= cus; }
+
 template <typename ET, int NP, int NO, int W, int S, bool kBack>
 hipError_t launch_walk_of(const ChunkArgs &a, hipStream_t s) {
     const int parts = 8 / W;
@@ -302,12 +307,8 @@ hipError_t launch_walk_of(const ChunkArgs &a, hipStream_t s) {
 }
 template <typename ET, int NP, int NO, int S, bool kBack>
 hipError_t launch_walk(const ChunkArgs &a, hipStream_t s) {
-    const int64_t heads = static_cast<int64_t>(a.s.B) * a.s.Hv;
-    const int cus = device_cus();
-    if (heads * 8 <= cus) return launch_walk_of<ET, NP, NO, 1, S, kBack>(a, s);
-    if (heads * 4 <= cus) return launch_walk_of<ET, NP, NO, 2, S, kBack>(a, s);
-    if (heads * 2 <= cus) return launch_walk_of<ET, NP, NO, 4, S, kBack>(a, s);
-    return launch_walk_of<ET, NP, NO, 8, S, kBack>(a, s);
+    const bool halves = halves_heads(static_cast<int64_t>(a.s.B) * a.s.Hv, device_cus());
+    return halves ? launch_walk_of<ET, NP, NO, 4, S, kBack>(a, s) : launch_walk_of<ET, NP, NO, 8, S, kBack>(a, s);
 }
 
 }  // namespace
