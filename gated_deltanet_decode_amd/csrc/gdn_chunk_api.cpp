@@ -22,8 +22,8 @@ using gdn::fail;
 using gdn::hip_status;
 using gdn::type_bytes;
 
-// Each launch has at most 512 work-items a head of the state's rows, or 256 a
-// chunk place and head, and the dispatch counts them in 32 bits.
+// Each launch has at most 512 work-items a head, or a chunk place and head, and the
+// dispatch counts them in 32 bits.
 constexpr int64_t kMaxHeads = 8388607, kMaxPlaces = 8388607;
 
 int check_packed(const gdn_dims *d, int32_t B, int32_t tokens, int32_t type, const int32_t *offsets) {

@@ -505,13 +505,13 @@ int gdn_pair_commit(const gdn_dims *dims, int32_t layers, int32_t B, const int32
  *            to, not including, offsets[b+1] (none: its state is handed on).
  *            NULL: B sequences of tokens / B.  Rows that belong to no sequence
  *            are neither read nor written.  Offsets must not descend; ones
- *            outside [0, tokens] count as the nearer end, and one below the one
- *            before it as equal to it (tokens that two sequences then share hold
- *            either's output).
+ *            outside [0, tokens] count as the nearer end.  Where they do descend
+ *            no access leaves the tensors, but what the sequences get is
+ *            undefined.
  *   slots    [B] int32, optional: the states of sequence b are those at slots[b];
  *            a sequence whose slot is outside [0, n_slots) is left out, and
- *            none of its rows is written (a padded batch).  Two sequences with
- *            one slot leave the state of either.  NULL: slot b, n_slots = B.
+ *            none of its rows is written (a padded batch).  No two sequences
+ *            may share a slot (their outputs and its state are undefined).  NULL: slot b, n_slots = B.
  *   state    [n_slots][n_v_heads][d_v][d_k]  before each sequence's first token
  *   state_out  the same shape: after its last; may be `state` itself (in
  *            place).  Slots that no sequence names are not written.
@@ -562,7 +562,7 @@ size_t gdn_chunk_workspace_bytes(const gdn_dims *dims, int32_t B, int32_t tokens
  * there (its exp is 0 either way).  Rows of no sequence are not written.
  *   workspace  gdn_chunk_backward_workspace_bytes(dims, B, tokens, type) bytes:
  *              the states that enter and the gradients that leave every chunk
- *              (260 KB a chunk of 64 tokens and value head)
+ *              (269 KiB a chunk of 64 tokens and value head)
  */
 int gdn_chunk_backward(const gdn_dims *dims, int32_t B, int32_t tokens, int32_t type, const void *q,
                        const void *k, const void *v, const float *beta, const float *gate,
