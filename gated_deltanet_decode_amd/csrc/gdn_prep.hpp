@@ -10,6 +10,12 @@
 // costs the later ones no accuracy.  T is formed by blocks of 16: the diagonal
 // ones by substitution, a column a lane, the others from them by float32
 // matrix products, column of blocks by column.
+//
+// The vector units bound it (exponentials, cutting results into planes, the 16
+// dependent steps of a substitution), then the 33 KB that it writes a chunk and value
+// head: 8 x 4096 tokens bf16, 32 value heads, 176 us, 3.1 TB/s of blocks; the 4 chunks of
+// 200 tokens 10 us.  T in float32, cut by each workgroup of the walk: the walk 10 %
+// slower.
 #pragma once
 
 #include <hip/hip_runtime.h>

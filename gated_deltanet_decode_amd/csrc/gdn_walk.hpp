@@ -16,6 +16,11 @@
 // an operand's lane needs (gdn_mma.hpp).  What all rows share (K, Q, T, P) comes
 // through LDS once a workgroup.  The state and whatever feeds it are kept to
 // binary32: three planes of M and Delta against the planes of K.
+//
+// The chain of products a chunk bounds it, K M^T to X to Delta to M', each waiting for
+// the one before: 8 x 4096 tokens bf16, 32 value heads, 512 us with the matrix units 57 %
+// busy (clock 1.7 GHz); 1 x 4096 about 230 us, 3.6 us a chunk.  Waiting for every
+// fetch and store at a chunk's end, and without the swizzle of columns: 640 us.
 #pragma once
 
 #include "gdn_prep.hpp"
