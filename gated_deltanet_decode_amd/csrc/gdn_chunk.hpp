@@ -83,7 +83,7 @@ struct BackArgs {
     float *dgate;
     // workspace
     char *back;                      // as within: T read along its columns, P transposed, vec
-    double *gsum;                    // [place][Hv][64] running sums of the gates
+    double *gsum;                    // [place][Hv][64] running sums of the gates, times log2 e
     float *dstates;                  // [place][Hv][dv][dk] that leave the chunks
     float *r;                        // [place][Hv][64][dv]
     float *du;                       // [place][Hv][8] sums of delta * (gradient of M' k) over 16 rows

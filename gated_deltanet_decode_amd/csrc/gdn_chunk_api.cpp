@@ -22,9 +22,10 @@ using gdn::fail;
 using gdn::hip_status;
 using gdn::type_bytes;
 
-// Each launch has at most 512 work-items a head, or a chunk place and head, and the
-// dispatch counts them in 32 bits.
-constexpr int64_t kMaxHeads = 8388607, kMaxPlaces = 8388607;
+// Each launch has at most 1024 work-items a head (and as many for up to seven key
+// heads' value heads more), or 512 a chunk place and head, and the dispatch counts them
+// in 32 bits.
+constexpr int64_t kMaxHeads = 3735551, kMaxPlaces = 8388607;
 
 int check_packed(const gdn_dims *d, int32_t B, int32_t tokens, int32_t type, const int32_t *offsets) {
     GDN_TRY(gdn::check_dims(d));
@@ -261,9 +262,6 @@ int gdn_decode(const gdn_dims *dims, int32_t B, int32_t tokens, int32_t type, co
     clear_error();
     GDN_TRY(check_packed(dims, B, tokens, type, offsets));
     GDN_TRY(check_slots(slots, n_slots, B));
-    if (static_cast<int64_t>(B) * dims->n_v_heads > kMaxHeads / 2)   // 1024 work-items a head
-        return fail(GDN_ERR_SHAPE, "B * n_v_heads = %lld exceeds %lld", (long long)B * dims->n_v_heads,
-                    (long long)kMaxHeads / 2);
     GDN_TRY(check_tensors(dims, B, tokens, type, q, k, v, beta, gate, offsets, slots, n_slots, state, state_out,
                           out, true, nullptr));
     gdn::DecodeArgs a{};

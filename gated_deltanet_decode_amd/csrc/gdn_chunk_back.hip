@@ -75,8 +75,8 @@ __device__ __forceinline__ void load_planes(const ChunkArgs &a, int which, char 
 }
 
 // Along the sequences in reverse, 16 rows of G a wave as k_walk has rows of M, and bound
-// as that is: 8 ragged sequences of up to 4096 tokens bf16 667 us (19 thousand tokens; k_walk
-// with what the backward pass keeps of it 610), 1 x 333 36 us.
+// as that is: 8 ragged sequences of up to 4096 tokens bf16 632 us (19 thousand tokens; k_walk
+// with what the backward pass keeps of it 596), 1 x 333 36 us.
 template <typename ET, int NP, int W, int S>
 __global__ __launch_bounds__(64 * W) void k_back(BackArgs a, int parts) {
     typedef typename ET::bits bits;
@@ -86,12 +86,9 @@ __global__ __launch_bounds__(64 * W) void k_back(BackArgs a, int parts) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
     const Packed &s = a.f.s;
-    const int Hv = s.Hv, Hk = s.Hk;
-    const int id = (blockIdx.x & 7) * static_cast<int>(gridDim.x >> 3) + (blockIdx.x >> 3);
-    const int part = id % parts, hh = id / parts;
-    const int b = hh / Hv;
-    if (b >= s.B) return;
-    const int kh = (hh - b * Hv) / (Hv / Hk), h = kh + (hh - b * Hv) % (Hv / Hk) * Hk;
+    const int Hv = s.Hv;
+    int b, kh, h, part;
+    if (!workgroup_at(s, parts, b, kh, h, part)) return;
     const Span sp = span_of(s, b);
     const int chunks = (sp.len + kChunk - 1) / kChunk;
     const int dv = (part * W + wave) * 16 + r;
@@ -269,7 +266,7 @@ __global__ __launch_bounds__(64 * W) void k_back(BackArgs a, int parts) {
 // from memory as operands, and through LDS for the other waves; the slabs of M and G
 // are cut into planes in LDS and read by columns; the next slab, of the next head too,
 // is on its way meanwhile.  Cutting into planes and the matrix instructions bound it,
-// about half each; 8 ragged sequences of up to 4096 tokens, 32 value heads: 826 us
+// about half each; 8 ragged sequences of up to 4096 tokens, 32 value heads: 806 us
 // (four waves with whole rows of dk, products of rows scaled ahead: 1130).
 template <typename ET, int NP, int NO>
 __global__ __launch_bounds__(512) void k_grad(BackArgs a) {
@@ -307,11 +304,7 @@ __global__ __launch_bounds__(512) void k_grad(BackArgs a) {
         const int unit = which == 0 ? w + 2 * half : which == 1 ? 6 + w + 4 * (1 - half) : 12 + 2 * w + half;
         return ld + (unit * NO + m) * 1024 + lane * 16;
     };
-    // (16-bit results round far above the hardware exponential's error)
-    const auto decay = [](double x) {
-        const float d = static_cast<float>(x);
-        return NO == 2 ? __builtin_amdgcn_exp2f(d * 1.44269504f) : expf(d);
-    };
+    const auto decay = [](double x) { return exp_2(x); };
 
     f4 r0, r1, d0, d1, m0, m1, g0, g1;
     typename Rows<ET>::Eight o, v;
@@ -573,8 +566,7 @@ __global__ __launch_bounds__(512) void k_grad(BackArgs a) {
 template <typename ET, int NP, int W, int S>
 hipError_t launch_back_of(const BackArgs &a, hipStream_t s) {
     const int parts = 8 / W;
-    const int64_t wgs = static_cast<int64_t>(a.f.s.B) * a.f.s.Hv * parts;
-    k_back<ET, NP, W, S><<<dim3(static_cast<unsigned>((wgs + 7) / 8 * 8)), dim3(64 * W), 0, s>>>(a, parts);
+    k_back<ET, NP, W, S><<<dim3(walk_grid(a.f.s, parts)), dim3(64 * W), 0, s>>>(a, parts);
     return hipGetLastError();
 }
 template <typename ET, int NP, int S>

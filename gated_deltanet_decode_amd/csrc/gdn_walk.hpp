@@ -18,7 +18,7 @@
 // binary32: three planes of M and Delta against the planes of K.
 //
 // The chain of products a chunk bounds it, K M^T to X to Delta to M', each waiting for
-// the one before: 8 x 4096 tokens bf16, 32 value heads, 512 us with the matrix units 57 %
+// the one before: 8 x 4096 tokens bf16, 32 value heads, 470 us with the matrix units 60 %
 // busy (clock 1.7 GHz); 1 x 4096 about 230 us, 3.6 us a chunk.  Waiting for every
 // fetch and store at a chunk's end, and without the swizzle of columns: 640 us.
 #pragma once
@@ -109,6 +109,24 @@ __device__ __forceinline__ void fetch_block(const char *block, char *to, int wav
 // outputs see; S buffers of a chunk's operands.  For the backward pass (kBack) the
 // states that enter each chunk and the corrections are kept, and the outputs
 // only meet their gradient: od is the sum over the wave's rows of out * d_out.
+// A workgroup's sequence, heads and part of its head's rows.  The workgroups of a key
+// head are neighbours on one XCD (ids modulo 8), the key heads of a sequence spread
+// over all: 8 x 4096 tokens bf16 554 us for the whole of gdn_chunk, with a sequence on
+// one XCD 577.
+__device__ __forceinline__ bool workgroup_at(const Packed &s, int parts, int &b, int &kh, int &h, int &part) {
+    const int per = parts * (s.Hv / s.Hk), at = static_cast<int>(blockIdx.x >> 3) % per;
+    const int unit = static_cast<int>(blockIdx.x >> 3) / per * 8 + (blockIdx.x & 7);
+    b = unit / s.Hk;
+    kh = unit - b * s.Hk;
+    part = at % parts;
+    h = kh + at / parts * s.Hk;
+    return b < s.B;
+}
+inline unsigned walk_grid(const Packed &s, int parts) {
+    const int64_t units = static_cast<int64_t>(s.B) * s.Hk;
+    return static_cast<unsigned>((units + 7) / 8 * 8 * parts * (s.Hv / s.Hk));
+}
+
 template <typename ET, int NP, int NO, int W, int S, bool kBack>
 __global__ __launch_bounds__(64 * W) void k_walk(ChunkArgs a, int parts) {
     typedef typename ET::bits bits;
@@ -117,14 +135,9 @@ __global__ __launch_bounds__(64 * W) void k_walk(ChunkArgs a, int parts) {
     __shared__ alignas(1024) char buf0[L::kBytes], buf1[S > 1 ? L::kBytes : 16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
-    const int Hv = a.s.Hv, Hk = a.s.Hk;
-    // Each XCD (ids modulo 8) takes a run of neighbours: the parts of a head, then the
-    // heads that share a key head.
-    const int id = (blockIdx.x & 7) * static_cast<int>(gridDim.x >> 3) + (blockIdx.x >> 3);
-    const int part = id % parts, hh = id / parts;
-    const int b = hh / Hv;
-    if (b >= a.s.B) return;
-    const int kh = (hh - b * Hv) / (Hv / Hk), h = kh + (hh - b * Hv) % (Hv / Hk) * Hk;
+    const int Hv = a.s.Hv;
+    int b, kh, h, part;
+    if (!workgroup_at(a.s, parts, b, kh, h, part)) return;
     const int slot = slot_of(a.s, b);
     if (slot < 0) return;
     const Span sp = span_of(a.s, b);
@@ -306,8 +319,7 @@ constexpr bool halves_heads(int64_t heads, int cus) { return 2 * heads <= cus; }
 template <typename ET, int NP, int NO, int W, int S, bool kBack>
 hipError_t launch_walk_of(const ChunkArgs &a, hipStream_t s) {
     const int parts = 8 / W;
-    const int64_t wgs = static_cast<int64_t>(a.s.B) * a.s.Hv * parts;
-    k_walk<ET, NP, NO, W, S, kBack><<<dim3(static_cast<unsigned>((wgs + 7) / 8 * 8)), dim3(64 * W), 0, s>>>(a, parts);
+    k_walk<ET, NP, NO, W, S, kBack><<<dim3(walk_grid(a.s, parts)), dim3(64 * W), 0, s>>>(a, parts);
     return hipGetLastError();
 }
 template <typename ET, int NP, int NO, int S, bool kBack>

@@ -517,8 +517,8 @@ int gdn_pair_commit(const gdn_dims *dims, int32_t layers, int32_t B, const int32
  *            place).  Slots that no sequence names are not written.
  * Alignment: q, k, v, out, the states and the workspace 16 bytes, the others 4.
  * Limits (GDN_ERR_SHAPE beyond): B, tokens >= 1, n_v_heads <= 65535, B *
- * n_v_heads <= 8388607 (gdn_decode: 4194303), and for gdn_chunk (tokens / 64 +
- * B) * n_v_heads <= 8388607.
+ * n_v_heads <= 3735551, and for gdn_chunk (tokens / 64 + B) * n_v_heads <=
+ * 8388607.
  *
  * gdn_chunk takes 64 tokens at a time: the corrections of a chunk's tokens are
  * the solution of a triangular system, and everything else is matrix products.

@@ -83,6 +83,15 @@ def test_gates(g, gate):
     check(x, backward(g, x), torch.float32)
 
 
+def test_slight_decays(g):
+    """Gates from nothing at all over what float64 just tells from it beside 1 to strong."""
+    x = rr.inputs([130, 64, 1, 70], 4, 2, torch.float32, 31)
+    kinds = torch.tensor([0.0, -0.0, -1e-38, -2.0**-60, -2.0**-54, -1e-12, -1e-5, -0.3, -1.0, -50.3], device="cuda")
+    x["gate"] = kinds[torch.randint(0, len(kinds), x["gate"].shape, generator=torch.Generator().manual_seed(3)).cuda()]
+    x["gate"][:64] = -2.0**-60                            # a chunk of nothing else
+    check(x, backward(g, x), torch.float32)
+
+
 @pytest.mark.parametrize("dtype", rr.TYPES.values(), ids=rr.TYPES)
 def test_betas(g, dtype):
     """Tokens that write nothing still have a gradient of beta."""
