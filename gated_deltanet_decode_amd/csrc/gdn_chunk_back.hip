@@ -266,8 +266,8 @@ __global__ __launch_bounds__(64 * W) void k_back(BackArgs a, int parts) {
 // from memory as operands, and through LDS for the other waves; the slabs of M and G
 // are cut into planes in LDS and read by columns; the next slab, of the next head too,
 // is on its way meanwhile.  Cutting into planes and the matrix instructions bound it,
-// about half each; 8 ragged sequences of up to 4096 tokens, 32 value heads: 806 us
-// (four waves with whole rows of dk, products of rows scaled ahead: 1130).
+// about half each; 8 ragged sequences of up to 4096 tokens, 32 value heads: 774 us
+// (one buffer of slabs 806, four waves with whole rows of dk, products of rows scaled ahead: 1130).
 template <typename ET, int NP, int NO>
 __global__ __launch_bounds__(512) void k_grad(BackArgs a) {
     constexpr int kRow = 64;                              // bytes of a token's slab of a plane
@@ -278,14 +278,16 @@ __global__ __launch_bounds__(512) void k_grad(BackArgs a) {
     constexpr int kK = NP * kPlaneBytes, kSlab = 3 * NO * kTok + 2 * NO * kMat, kPass = 20 * NO * 1024;
     constexpr bool kStays = NP < 3;
     constexpr int kTurn = kStays ? 2 * kK : kK, kQ = kStays ? kK : kK + kPass;
-    constexpr int kAll = kStays ? kTurn + (kSlab > kPass ? kSlab : kPass) : kTurn + (kSlab > kPass + kK ? kSlab : kPass + kK);
+    constexpr int kBuffers = NP == 1 ? 2 : 1;             // of slabs
+    constexpr int kAll = kStays ? kTurn + kBuffers * (kSlab > kPass ? kSlab : kPass)
+                                : kTurn + (kSlab > kPass + kK ? kSlab : kPass + kK);
+    static_assert(kBuffers == 1 || kPass <= kSlab, "F and E fit the buffer that is not being read");
     __shared__ alignas(16) char lds[kAll];
     __shared__ double gs[kChunk], part[8];
     __shared__ float vec[kVecFloats], dots[2][kChunk], ods[8][kChunk], dus[8];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4, w = wave & 3, p = wave >> 2;
-    // LDS of Delta, of d_out or R, which is the half's own, of M and of G
-    char *const ld = lds + kTurn, *const lx = ld + (1 + p) * NO * kTok, *const lm = ld + 3 * NO * kTok, *const lg = lm + NO * kMat;
+    char *const turn0 = lds + kTurn;
     const Packed &s = a.f.s;
     const int Hv = s.Hv, Hk = s.Hk;
     const int place = blockIdx.x / Hk, kh = blockIdx.x - place * Hk;
@@ -302,7 +304,7 @@ __global__ __launch_bounds__(512) void k_grad(BackArgs a) {
     // (the halves that are there)
     const auto pass_at = [&](int lane, int which, int half, int m) {
         const int unit = which == 0 ? w + 2 * half : which == 1 ? 6 + w + 4 * (1 - half) : 12 + 2 * w + half;
-        return ld + (unit * NO + m) * 1024 + lane * 16;
+        return turn0 + (unit * NO + m) * 1024 + lane * 16;
     };
     const auto decay = [](double x) { return exp_2(x); };
 
@@ -354,8 +356,13 @@ __global__ __launch_bounds__(512) void k_grad(BackArgs a) {
         for (int slab = 0; slab < 4; ++slab) {
             const int lane = here(threadIdx.x) & 63, r = lane & 15, g = lane >> 4, tok = w * 16 + r;
             u4 op[NO] = {}, rp[NO], dp[NO];
-            wait_lds();
-            meet();                                       // the last slab, or F and E, is read
+            // LDS of Delta, of d_out or R, which is the half's own, of M and of G
+            char *const ld = turn0 + (kBuffers == 2 ? slab & 1 : 0) * kSlab, *const lx = ld + (1 + p) * NO * kTok,
+                 *const lm = ld + 3 * NO * kTok, *const lg = lm + NO * kMat;
+            if (kBuffers == 1 || slab == 0) {
+                wait_lds();
+                meet();                                   // the last slab, or F and E, is read
+            }
             {
                 const int mr = here(threadIdx.x) >> 4, mc = here(threadIdx.x) & 15;  // this thread's piece of M and G
                 u4 mp[NO], gp[NO];
@@ -436,8 +443,10 @@ __global__ __launch_bounds__(512) void k_grad(BackArgs a) {
                 dk[t][e] = fmaf(fall, dg[t][e], fmaf(-beta * rise, rm[t][e], dk[t][e]));
             }
         }
-        wait_lds();
-        meet();                                           // the slabs are read: F and E take their place
+        if (kBuffers == 1) {
+            wait_lds();
+            meet();                                       // the slabs are read: F and E take their place
+        }
         if (!kStays) load_planes<ET, NP, 512>(a.f, 1, lds + kQ, place, t0, n, kh);
         // decays and masks
         const double gt = gs[tok];
