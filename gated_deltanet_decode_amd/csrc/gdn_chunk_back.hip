@@ -265,8 +265,8 @@ __global__ __launch_bounds__(64 * W) void k_back(BackArgs a, int parts) {
 // dv run in slabs of 32: a wave's own rows of R, Delta and d_out come straight
 // from memory as operands, and through LDS for the other waves; the slabs of M and G
 // are cut into planes in LDS and read by columns; the next slab, of the next head too,
-// is on its way meanwhile.  Cutting into planes and the matrix instructions bound it,
-// about half each; 8 ragged sequences of up to 4096 tokens, 32 value heads: 774 us
+// is on its way meanwhile.  The vector units (cutting, 39 % busy), the matrix units (17 %)
+// and waiting for memory and each other bound it; 8 ragged sequences of up to 4096 tokens, 32 value heads: 774 us
 // (one buffer of slabs 806, four waves with whole rows of dk, products of rows scaled ahead: 1130).
 template <typename ET, int NP, int NO>
 __global__ __launch_bounds__(512) void k_grad(BackArgs a) {

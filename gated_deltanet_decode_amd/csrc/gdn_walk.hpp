@@ -18,8 +18,8 @@
 // binary32: three planes of M and Delta against the planes of K.
 //
 // The chain of products a chunk bounds it, K M^T to X to Delta to M', each waiting for
-// the one before: 8 x 4096 tokens bf16, 32 value heads, 470 us with the matrix units 60 %
-// busy (clock 1.7 GHz); 1 x 4096 about 230 us, 3.6 us a chunk.  Waiting for every
+// the one before: 8 x 4096 tokens bf16, 32 value heads, 470 us with the matrix units 49 %
+// and the vector units 50 % busy, which overlap little (clock 1.55 GHz); 1 x 4096 about 230 us, 3.6 us a chunk.  Waiting for every
 // fetch and store at a chunk's end, and without the swizzle of columns: 640 us.
 #pragma once
 
