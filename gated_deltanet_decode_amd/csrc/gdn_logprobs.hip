@@ -21,9 +21,10 @@
 // One pass over memory, a row in as many units as give every compute unit four; a
 // second launch joins the units where there are several.  The exponentials and their
 // sums bound it, eight instructions an entry of which one takes four times as
-// long: 1024 rows x 131071 bf16 66 us (4.0 TB/s), the best 20 with them 85 (two units a
-// row and their join: 75 and 94); 32 x 128000 with 20 16 us; the next vectors on
-// their way during the sums: no gain.
+// long: 1024 rows x 131071 bf16 62 us (4.3 TB/s), the best 20 with them 82 (vectors from
+// the row's own start, unaligned: 66 and 85; two units a row and their join: 75 and
+// 94); 32 x 128000 with 20 16 us; the next vectors on their way during the sums: no
+// gain.
 #include "gdn.h"
 #include "gdn_elem.hpp"
 #include "gdn_launch.hpp"
@@ -83,17 +84,17 @@ __device__ __forceinline__ Sums joined(const Sums &s) {
     return c;
 }
 
-// Entries v.. of a row, N of them; those past its end or before v are -inf.
+// Entries v.. of a row, N of them; those outside [first, end) are -inf.
 template <typename LT, int N>
-__device__ __forceinline__ void load(const typename LT::bits *row, int64_t v, int V, float (&x)[N]) {
+__device__ __forceinline__ void load(const typename LT::bits *row, int64_t v, int first, int64_t end, float (&x)[N]) {
     typedef typename LT::bits bits;
-    if (v + N <= V) {
+    if (v >= first && v + N <= end) {
         const auto w = Pack<bits, N>::load(row + v);
 #pragma unroll
         for (int j = 0; j < N; ++j) x[j] = LT::get(w[j]);
     } else {
 #pragma unroll
-        for (int j = 0; j < N; ++j) x[j] = v + j < V ? LT::get(row[v + j]) : -__builtin_inff();
+        for (int j = 0; j < N; ++j) x[j] = v + j >= first && v + j < end ? LT::get(row[v + j]) : -__builtin_inff();
     }
 }
 
@@ -153,9 +154,13 @@ __global__ __launch_bounds__(kT) void k_logprobs(LogprobsArgs a, int unit, int u
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t row = kOne ? blockIdx.x : blockIdx.x / units;
     const int u = kOne ? 0 : static_cast<int>(blockIdx.x - row * units);
+    // Counted from the 16 bytes that the row begins in, so that vectors are aligned: the
+    // first `skip` entries are not the row's.
     const bits *x = static_cast<const bits *>(a.logits) + row * a.ld;
+    const int skip = static_cast<int>(reinterpret_cast<uintptr_t>(x) / sizeof(bits) % N);
+    x -= skip;
     const int64_t v0 = static_cast<int64_t>(u) * unit;
-    const int end = static_cast<int>(min(static_cast<int64_t>(a.V), v0 + unit));
+    const int end = static_cast<int>(min(static_cast<int64_t>(a.V) + skip, v0 + unit));
     const int turns = static_cast<int>((end - v0 + kT * N - 1) / (kT * N));   // vectors of a thread
 
     float m = kLeast, z = 0.0f, t = 0.0f;
@@ -184,6 +189,15 @@ __global__ __launch_bounds__(kT) void k_logprobs(LogprobsArgs a, int unit, int u
         }
     };
     int i = 0;
+    const auto slow = [&](int i) {                        // a vector that may reach over the row's ends
+        float y[N];
+        load<LT, N>(x, v0 + (static_cast<int64_t>(i) * kT + tid) * N, skip, end, y);
+        float top = y[0];
+#pragma unroll
+        for (int j = 1; j < N; ++j) top = fmaxf(top, y[j]);
+        add(top, N, [&](int j) { return y[j]; });
+    };
+    if (v0 < skip) slow(i++);
     for (; v0 + static_cast<int64_t>(i + kAhead) * (kT * N) <= end; i += kAhead) {
         typename Pack<bits, N>::vec w[kAhead];
 #pragma unroll
@@ -195,14 +209,7 @@ __global__ __launch_bounds__(kT) void k_logprobs(LogprobsArgs a, int unit, int u
             for (int j = 0; j < N; ++j) top = fmaxf(top, LT::get(w[k][j]));
         add(top, kAhead * N, [&](int j) { return LT::get(w[j / N][j % N]); });
     }
-    for (; i < turns; ++i) {
-        float y[N];
-        load<LT, N>(x, v0 + (static_cast<int64_t>(i) * kT + tid) * N, end, y);
-        float top = y[0];
-#pragma unroll
-        for (int j = 1; j < N; ++j) top = fmaxf(top, y[j]);
-        add(top, N, [&](int j) { return y[j]; });
-    }
+    for (; i < turns; ++i) slow(i);
     // groups' maxima; the best `top` entries
     if (a.top > 0) {
         float gm = fmaxf(m, __shfl_xor(m, 1));
@@ -234,12 +241,12 @@ __global__ __launch_bounds__(kT) void k_logprobs(LogprobsArgs a, int unit, int u
             const int turn = w / listed;
             const int64_t v = v0 + (static_cast<int64_t>(turn) * kT + threads[w - turn * listed]) * N;
             float y[N];
-            load<LT, N>(x, v, end, y);
+            load<LT, N>(x, v, skip, end, y);
 #pragma unroll
             for (int j = 0; j < N; ++j)
                 if (y[j] >= kLeast && order(y[j]) >= bound) {
                     const int at = atomicAdd(&n_list, 1);
-                    if (at < kList) list[at] = key_of(y[j], static_cast<int>(v + j));
+                    if (at < kList) list[at] = key_of(y[j], static_cast<int>(v + j) - skip);
                 }
         }
         __syncthreads();
@@ -259,10 +266,10 @@ __global__ __launch_bounds__(kT) void k_logprobs(LogprobsArgs a, int unit, int u
                 for (int w = 0; w < turns; ++w) {
                     const int64_t v = v0 + (static_cast<int64_t>(w) * kT + tid) * N;
                     float y[N];
-                    load<LT, N>(x, v, end, y);
+                    load<LT, N>(x, v, skip, end, y);
 #pragma unroll
                     for (int j = 0; j < N; ++j) {
-                        const uint64_t c = y[j] >= kLeast ? key_of(y[j], static_cast<int>(v + j)) : kNone;
+                        const uint64_t c = y[j] >= kLeast ? key_of(y[j], static_cast<int>(v + j) - skip) : kNone;
                         key = c < last && c > key ? c : key;
                     }
                 }
@@ -348,7 +355,8 @@ __global__ __launch_bounds__(kT) void k_join(LogprobsArgs a, int units) {
 
 template <typename LT, int N>
 hipError_t launch(const LogprobsArgs &a, int64_t units, hipStream_t s) {
-    const int unit = static_cast<int>(((a.V + units - 1) / units + N - 1) / N * N);
+    // (a row's first vector may begin N - 1 entries before it)
+    const int unit = static_cast<int>(((a.V + N - 1 + units - 1) / units + N - 1) / N * N);
     if (units == 1) {
         k_logprobs<LT, N, true><<<dim3(static_cast<unsigned>(a.rows)), dim3(kT), 0, s>>>(a, unit, 1);
         return hipGetLastError();
