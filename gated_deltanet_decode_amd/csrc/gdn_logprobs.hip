@@ -7,10 +7,11 @@
 // A thread keeps its own m and rescales Z and T when it grows; threads are joined
 // in binary64, so that log p of a nearly certain token keeps its digits.  In
 // powers of two, with c the binary32 number next to log2 e: each term is
-// 2^(c x - R), one fma and one exponential, where R is c m rounded to binary32 (or
-// c m itself where m is so large that c x would overflow).  For that the
-// reference is R / c in place of m; and as c log 2 = 1 - e, e = 1.3e-8, log Z lacks
-// e times the mean of x - R / c, which T gives.
+// 2^(c x - R), one fma and one exponential, where R is c m rounded to binary32.  From
+// |m| = 2^20 on, where that rounding would no longer be small beside 1 (from 2^31 on it
+// may pass 2^7: the largest term overflows or vanishes), R is c m itself and a term
+// 2^(c (x - m)).  The reference is then R / c in place of m; and as c log 2 = 1 - e,
+// e = 1.3e-8, log Z lacks e times the mean of x - R / c, which T gives.
 //
 // The most likely tokens need no work per entry: the K-th largest of the maxima of
 // groups (the entries of four neighbouring threads) bounds the K-th largest entry
@@ -39,7 +40,7 @@ constexpr int kAhead = 4;                    // vectors that a thread fetches at
 constexpr int kList = 512;                   // entries that are ranked at most
 constexpr float kLog2e = 1.44269504088896f;
 constexpr double kLn2 = 0.693147180559945309417, kLacks = 1.0 - kLn2 * kLog2e;
-constexpr float kLarge = 0x1p100f;
+constexpr float kLarge = 0x1p20f;            // R of a smaller m is off c m by 2^-4 at most
 constexpr float kLeast = -3.402823466e38f;
 
 // Orders as the values, -0 as 0; 0 is below every float's.
