@@ -126,7 +126,8 @@ __global__ __launch_bounds__(64 * W) void k_back(BackArgs a, int parts) {
         for (int i = 0; i < 16; ++i)
             dl[i] = a.f.delta[(ph * kChunk + 16 * (i / 4) + 4 * g + i % 4) * kHeadDim + dv];
         if (S == 1) {
-            meet();
+            wait_lds();
+            meet();                                       // the buffer is read
             fetch(cur, c);
             wait_all<0>();
         } else {

@@ -177,6 +177,7 @@ __global__ __launch_bounds__(64 * W) void k_walk(ChunkArgs a, int parts) {
             for (int t = 0; t < 8; ++t) *reinterpret_cast<f4 *>(to + 32 * (t / 2) + 4 * (t % 2)) = M[t];
         }
         if (S == 1) {
+            wait_lds();
             meet();                                       // the buffer is read
             fetch(cur, c);
             wait_all<0>();
