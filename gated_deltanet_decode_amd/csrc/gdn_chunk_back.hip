@@ -192,6 +192,7 @@ __global__ __launch_bounds__(64 * W) void k_back(BackArgs a, int parts) {
         planes_of<3>(dd[0], dd[1], xp);
         f4 (&R0)[2] = *reinterpret_cast<f4 (*)[2]>(&R[0]);
         mma_planes<2, true>(te, xp, R0);
+        if constexpr (S > 1) in_order();                  // the next chunk's fetches are ahead of what is counted
         const Rows<ET> dvr = rows_of(a.dv, c);
 #pragma unroll
         for (int jt = 0; jt < 4; ++jt) {

@@ -272,6 +272,7 @@ __global__ __launch_bounds__(64 * WK) void k_f8_ring(LinearF8Args a, int tiles_n
 #pragma unroll
             for (int j = 0; j < L; ++j)
                 fetch16(piece + j * 1024, j < 2 * TN ? pw : px, j < 2 * TN ? nw : nx, off[j], k0);
+            asm volatile("" ::: "memory");                // block after block, as they are waited for
         };
         auto step = [&](int8_t *piece, int i) {
             const int b = wave + i * WK;

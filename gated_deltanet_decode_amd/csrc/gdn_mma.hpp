@@ -112,6 +112,8 @@ __device__ __forceinline__ void wait_all() {
     __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));
     asm volatile("" ::: "memory");
 }
+// What is issued above stays ahead of what is issued below, so that a wait can count.
+__device__ __forceinline__ void in_order() { asm volatile("" ::: "memory"); }
 // None of this wave's LDS operations is still on its way.
 __device__ __forceinline__ void wait_lds() {
     asm volatile("" ::: "memory");

@@ -157,6 +157,7 @@ __global__ __launch_bounds__(64 * W) void k_walk(ChunkArgs a, int parts) {
         const int rows = min(kChunk, sp.len - c * kChunk);
         fetch_rows<ET, NP, W>(a, to + L::kK, to + L::kQ, place, sp.first + c * kChunk, rows, kh, wave, lane);
         fetch_block<within_bytes(NO), W>(a.within + (place * Hv + h) * within_bytes(NO), to + L::kT, wave, lane);
+        if constexpr (S > 1) in_order();                  // ahead of what is counted
     };
     auto rows_of = [&](const void *base, int c) {
         return Rows<ET>(base, static_cast<int64_t>(sp.first) + c * kChunk, min(kChunk, sp.len - c * kChunk), h, Hv);
