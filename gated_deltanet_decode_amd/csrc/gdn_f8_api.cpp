@@ -73,7 +73,8 @@ int gdn_linear_f8(int32_t M, int32_t K, const uint8_t *a, const float *a_scale, 
     GDN_TRY(check_type(out_type, "out_type"));
     if (M < 1) return fail(GDN_ERR_SHAPE, "M must be >= 1 (got %d)", M);
     // an offset into a tile's 256 rows stays below 2^31
-    if (K < 1 || K > 4194303) return fail(GDN_ERR_SHAPE, "K must be in [1, 4194303] (got %d)", K);
+    if (K < 1 || K > gdn::kTileMaxK)
+        return fail(GDN_ERR_SHAPE, "K must be in [1, %d] (got %d)", gdn::kTileMaxK, K);
     if (n_outs < 1 || n_outs > GDN_LINEAR_MAX_OUTS)
         return fail(GDN_ERR_SHAPE, "n_outs must be in [1, %d] (got %d)", GDN_LINEAR_MAX_OUTS, n_outs);
     if (!outs) return fail(GDN_ERR_NULL, "outs is NULL");

@@ -27,6 +27,7 @@ struct QuantArgs {
 constexpr int kQuantMaxThreads = 1024;
 
 constexpr int kLinearMaxOuts = 4;
+constexpr int kTileMaxK = 4194303;   // bytes of a row that a tile's offsets allow
 
 struct LinearArgs {
     const int8_t *a;

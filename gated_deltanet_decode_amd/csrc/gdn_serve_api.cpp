@@ -122,6 +122,7 @@ int gdn_linear_q8(int32_t M, int32_t K, const int8_t *a, const float *a_scale, c
     clear_error();
     GDN_TRY(check_type(out_type, "out_type"));
     if (M < 1) return fail(GDN_ERR_SHAPE, "M must be >= 1 (got %d)", M);
+    static_assert(131071 <= gdn::kTileMaxK, "");
     // |a w| <= 2^14, so the sum of 131071 products stays below 2^31
     if (K < 1 || K > 131071)
         return fail(GDN_ERR_SHAPE, "K must be in [1, 131071] (got %d)", K);

@@ -57,8 +57,9 @@ __device__ __forceinline__ void fetch16(int8_t *lds, const int8_t *base, uint32_
         off, k0, 0, 0);
 }
 
-// Bytes of `rows` rows of K bytes, as a buffer's size.  No offset into a tile
-// passes 2^31 (256 rows of at most 131071 bytes).
+// Bytes of `rows` rows of K bytes, as a buffer's size.  No offset into a tile's 256
+// rows passes 2^31.
+static_assert(int64_t{256} * kTileMaxK < INT64_C(0x7fffffff), "offsets into a tile");
 __device__ __forceinline__ uint32_t span(int rows, int K) {
     const int64_t b = static_cast<int64_t>(rows) * K;
     return b < 0x7fffffff ? static_cast<uint32_t>(b) : 0x7fffffffu;
