@@ -270,6 +270,7 @@ __global__ __launch_bounds__(64 * W) void k_back(BackArgs a, int parts) {
 // is on its way meanwhile.  The vector units (cutting, 39 % busy), the matrix units (17 %)
 // and waiting for memory and each other bound it; 8 ragged sequences of up to 4096 tokens, 32 value heads: 774 us
 // (one buffer of slabs 806, four waves with whole rows of dk, products of rows scaled ahead: 1130).
+// float32, three planes of everything, keeps 20 registers in scratch.
 template <typename ET, int NP, int NO>
 __global__ __launch_bounds__(512) void k_grad(BackArgs a) {
     constexpr int kRow = 64;                              // bytes of a token's slab of a plane

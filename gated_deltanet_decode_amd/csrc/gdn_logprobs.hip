@@ -20,12 +20,15 @@
 // the lower id: a 64-bit key of both.
 //
 // One pass over memory, a row in as many units as give every compute unit four; a
-// second launch joins the units where there are several.  The exponentials and their
-// sums bound it, eight instructions an entry of which one takes four times as
-// long: 1024 rows x 131071 bf16 62 us (4.3 TB/s), the best 20 with them 82 (vectors from
-// the row's own start, unaligned: 66 and 85; two units a row and their join: 75 and
+// second launch joins the units where there are several.  Memory and the vector units
+// bound it in turn: eight instructions an entry, one of them an exponential at a quarter of
+// the rate, keep these two thirds busy, and the waves wait for memory 72 % of their time.
+// 1024 rows x 131071 bf16 54-62 us (4.3-5.0 TB/s), the best 20 with them 73-82 (vectors
+// from the row's own start, unaligned: 66 and 85; two units a row and their join: 75 and
 // 94); 32 x 128000 with 20 16 us; the next vectors on their way during the sums: no
-// gain.
+// gain.  With top near 64 the bound is nearly the groups' smallest maximum, and more
+// entries than the list has pass it: then each of the best takes a pass of its own (top
+// 48 94 us, 63 119, 64 2400; 32 x 128000 20, 77 and 135).
 #include "gdn.h"
 #include "gdn_elem.hpp"
 #include "gdn_launch.hpp"

@@ -105,10 +105,6 @@ __device__ __forceinline__ void fetch_block(const char *block, char *to, int wav
         fetch16(to + (i * W + wave) * 1024, block, kBytes, (i * W + wave) * 1024 + lane * 16, 0);
 }
 
-// W waves, 16 rows of the state each.  NP planes of k and q, NO of what only the
-// outputs see; S buffers of a chunk's operands.  For the backward pass (kBack) the
-// states that enter each chunk and the corrections are kept, and the outputs
-// only meet their gradient: od is the sum over the wave's rows of out * d_out.
 // A workgroup's sequence, heads and part of its head's rows.  The workgroups of a key
 // head are neighbours on one XCD (ids modulo 8), the key heads of a sequence spread
 // over all: 8 x 4096 tokens bf16 554 us for the whole of gdn_chunk, with a sequence on
@@ -127,6 +123,10 @@ inline unsigned walk_grid(const Packed &s, int parts) {
     return static_cast<unsigned>((units + 7) / 8 * 8 * parts * (s.Hv / s.Hk));
 }
 
+// W waves, 16 rows of the state each.  NP planes of k and q, NO of what only the
+// outputs see; S buffers of a chunk's operands.  For the backward pass (kBack) the
+// states that enter each chunk and the corrections are kept, and the outputs
+// only meet their gradient: od is the sum over the wave's rows of out * d_out.
 template <typename ET, int NP, int NO, int W, int S, bool kBack>
 __global__ __launch_bounds__(64 * W) void k_walk(ChunkArgs a, int parts) {
     typedef typename ET::bits bits;

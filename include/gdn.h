@@ -511,21 +511,24 @@ int gdn_pair_commit(const gdn_dims *dims, int32_t layers, int32_t B, const int32
  *   slots    [B] int32, optional: the states of sequence b are those at slots[b];
  *            a sequence whose slot is outside [0, n_slots) is left out, and
  *            none of its rows is written (a padded batch).  No two sequences
- *            may share a slot (their outputs and its state are undefined).  NULL: slot b, n_slots = B.
+ *            may share a slot (their outputs and its state are undefined).
+ *            NULL: slot b, n_slots = B.
  *   state    [n_slots][n_v_heads][d_v][d_k]  before each sequence's first token
  *   state_out  the same shape: after its last; may be `state` itself (in
  *            place).  Slots that no sequence names are not written.
  * Alignment: q, k, v, out, the states and the workspace 16 bytes, the others 4.
  * Limits (GDN_ERR_SHAPE beyond): B, tokens >= 1, n_v_heads <= 65535, B *
- * n_v_heads <= 3735551, and for gdn_chunk (tokens / 64 + B) * n_v_heads <=
- * 8388607.
+ * n_v_heads <= 3735551, and for gdn_chunk tokens <= 2^31 - 65 and (tokens / 64 + B) *
+ * n_v_heads <= 8388607.
  *
  * gdn_chunk takes 64 tokens at a time: the corrections of a chunk's tokens are
  * the solution of a triangular system, and everything else is matrix products.
  * The state, the corrections and all sums are float32, and products whose result
  * enters the state or a float32 output are right to about 2^-23 of their terms;
- * outputs of 16 bits are rounded once, from sums right to 2^-15.  Results
- * depend neither on B nor on the other sequences.  A NaN or an infinity in a
+ * outputs of 16 bits are rounded once, from sums right to 2^-15.  Gates are summed
+ * over a chunk: one below -2^14 counts as -2^14 (its exp is 0 either way), and a sum
+ * that passes 88 overflows.  Results depend neither on B nor on the other
+ * sequences.  A NaN or an infinity in a
  * token reaches the state from its chunk on and may reach all outputs of its
  * chunk, those of the chunk's earlier tokens too.
  *   state      NULL: zeros
@@ -558,8 +561,10 @@ size_t gdn_chunk_workspace_bytes(const gdn_dims *dims, int32_t B, int32_t tokens
  * gradients are made of (right to about 2^-23 of the terms); 16-bit dq and dk are
  * rounded once, from sums right to 2^-15.  A beta of magnitude below 2^-60 counts as
  * 2^-60 in the corrections and as 0 in dv, which changes no gradient by a float32
- * rounding.  A sum of gates that falls by more than 2^14 in one token is held
- * there (its exp is 0 either way).  Rows of no sequence are not written.
+ * rounding.  Gates count as in gdn_chunk.  dgate is a sum over a chunk's tokens of
+ * d_out . out - dv . v: where these cancel, as for heads that forget at once, it keeps
+ * the error of float32 roundings of the products, however small it is itself.  Rows
+ * of no sequence are not written.
  *   workspace  gdn_chunk_backward_workspace_bytes(dims, B, tokens, type) bytes:
  *              the states that enter and the gradients that leave every chunk
  *              (269 KiB a chunk of 64 tokens and value head)
@@ -616,9 +621,9 @@ int gdn_quantize_f8(int32_t rows, int32_t n, int32_t block_rows, int32_t x_type,
  * products of eight neighbouring k to multiples of 2^-13 of the largest of the
  * eight before they add them (together less than 7 * 2^-13 of it, codes below 2^-6
  * counted as 2^-6 in it; of a sum of normally distributed codes 1.5e-5).  Ask for
- * float32 where outputs are small differences of large products.  The product of a row's and a channel's scale is formed
- * first, in float32.  The order of the blocks' sums depends on M, N and K; the same
- * call gives the same bits.
+ * float32 where outputs are small differences of large products.  The two scales'
+ * product is formed first, in float32.  The order of the blocks' sums depends on M, N
+ * and K; the same call gives the same bits.
  *   a        [M][K]  e4m3 bytes   a_scale  [M][ceil(K / 128)]              float32
  *   w        [N][K]  e4m3 bytes   w_scale  [ceil(N / 128)][ceil(K / 128)]  float32
  *   bias     [N]     float32, optional (NULL = none)
@@ -641,15 +646,16 @@ int gdn_linear_f8(int32_t M, int32_t K, const uint8_t *a, const float *a_scale, 
  * Z and the entropy's sum are float32 within a thread and binary64 across them;
  * the results round once.  Entries of -inf have probability 0 (a masked
  * vocabulary).  A row of nothing else gets logprob -inf and entropy 0; a row with
- * a NaN or +inf gets NaN, and -1 for the ids.
+ * a NaN or +inf gets NaN, and -1 for the ids.  The time hardly depends on top up to
+ * 56 or so; a top of 64 takes many passes over most rows (1024 x 131071 bf16 without
+ * top 57 us, 20: 74, 48: 94, 56: 96, 63: 119, 64: 2400).
  *   logits       rows of V entries of logit_type, ld >= V elements apart (a padded
  *                vocabulary is not read)
  *   tokens       [rows]       int32, optional; one outside [0, V) has logprob -inf
  *   logprob      [rows]       float32, given exactly when tokens is
  *   entropy      [rows]       float32, optional
- *   top_ids      [rows][top]  int32: by logit descending, equal ones by id
- *   top_logprobs [rows][top]  float32
- *                             ascending; both ignored where top is 0
+ *   top_ids      [rows][top]  int32: by logit descending, equal ones by id ascending
+ *   top_logprobs [rows][top]  float32, in the same order; both ignored where top is 0
  *   workspace    gdn_logprobs_workspace_bytes(rows, V, top) bytes, 16-byte
  *                aligned; NULL where that is 0.  Two calls that may overlap in
  *                time need one each.
