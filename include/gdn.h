@@ -646,9 +646,11 @@ int gdn_linear_f8(int32_t M, int32_t K, const uint8_t *a, const float *a_scale, 
  * Z and the entropy's sum are float32 within a thread and binary64 across them;
  * the results round once.  Entries of -inf have probability 0 (a masked
  * vocabulary).  A row of nothing else gets logprob -inf and entropy 0; a row with
- * a NaN or +inf gets NaN, and -1 for the ids.  The time hardly depends on top up to
- * 56 or so; a top of 64 takes many passes over most rows (1024 x 131071 bf16 without
- * top 57 us, 20: 74, 48: 94, 56: 96, 63: 119, 64: 2400).
+ * a NaN or +inf gets NaN, and -1 for the ids.  The time depends little on top up to
+ * 56 or so, but a top of 64 takes up to 64 more passes over most rows (1024 x 131071
+ * bf16 without top 57 us, 20: 74, 48: 94, 56: 96, 63: 119, 64: 2400), and so do rows
+ * in which some 500 finite entries tie for the last places (a finite mask that
+ * leaves fewer than top).
  *   logits       rows of V entries of logit_type, ld >= V elements apart (a padded
  *                vocabulary is not read)
  *   tokens       [rows]       int32, optional; one outside [0, V) has logprob -inf
